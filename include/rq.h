@@ -94,7 +94,8 @@ typedef enum {
   RQ_ERR_CAPACITY = 4,          /* tokens would exceed max_tokens, or buffer too small */
   RQ_ERR_WORKSPACE = 5,         /* workspace too small */
   RQ_ERR_CUDA = 6,              /* a CUDA runtime call failed */
-  RQ_ERR_DEVICE_TIMEOUT = 7     /* a kernel gave up waiting (see rq_decode_read_status) */
+  RQ_ERR_DEVICE_TIMEOUT = 7,    /* a kernel gave up waiting (see rq_decode_read_status) */
+  RQ_ERR_DEVICE_INDEX = 8       /* a kernel met a page, length or position out of range (paged calls) */
 } rq_status;
 
 /* Static, human-readable name of a status code.  Never NULL. */
@@ -339,6 +340,135 @@ rq_status rq_decode_attention_noalloc(rq_cache* cache, int layer, const void* q,
  *   it reflects the LAST call made on the device (from any thread).
  * Errors: RQ_ERR_INVALID_ARG (null pointer), RQ_ERR_CUDA. */
 rq_status rq_decode_noalloc_read_status(int* device_status);
+
+/* ------------------------------------------------------------ paged 16-bit cache
+ * Keys and values of one token stay as 16-bit rows in pages that any sequence
+ * may hold: the cache of what is not quantized -- prompts before
+ * rq_quantize_kv, layers with a sliding window, batches of sequences of
+ * different lengths, prompts that a batch shares.  The papers above have no
+ * counterpart.
+ *
+ * Two device tensors of pages (keys, values), each
+ *   [n_layers][n_pages][n_kv_heads][page_size][head_dim]
+ * of bf16 or fp16, contiguous, caller-owned.  Token t of a sequence lies in
+ * row t mod page_size of page page_table[sequence][t / page_size].
+ *
+ * A batch (rq_paged_batch) packs the new tokens of its sequences one behind
+ * another.  Sequence b has n_b = cu_new[b+1] - cu_new[b] new tokens (1 when
+ * cu_new is null) and holds kv_lens[b] tokens, the new ones included, so that
+ * new token i is token kv_lens[b] - n_b + i of its sequence.  The table, the
+ * lengths and cu_new are read on the device when the kernel runs: a captured
+ * graph may be replayed after they change.  Rows behind the last sequence
+ * (cu_new[n_seqs] < n_tokens) are not written.
+ *
+ * What the device finds out of range -- a page number outside [0, n_pages), a
+ * length outside [0, table_width * page_size], a position outside the table
+ * of angles, offsets outside [0, n_tokens] -- is not followed: the token is
+ * neither written nor seen, and the call's status word becomes
+ * RQ_ERR_DEVICE_INDEX (table entries of pages that no query sees are not
+ * looked at). */
+typedef struct {
+  int n_layers;   /* >= 1 */
+  int n_pages;    /* >= 1, of every layer */
+  int page_size;  /* tokens: 16, 32, 64 or 128 */
+  int n_q_heads;  /* multiple of n_kv_heads, ratio G in {1,2,4,8} */
+  int n_kv_heads; /* >= 1 */
+  int head_dim;   /* 64 or 128 */
+  int dtype;      /* of pages, queries, new tokens and outputs: 0 bf16, 1 fp16 */
+} rq_paged_config;
+
+typedef struct rq_paged_cache rq_paged_cache; /* opaque host handle */
+
+/* Bind caller-owned pages (16-byte aligned) of the current device to a new
+ * handle.  Reads and writes no device memory; the handle holds no lengths.
+ * Errors: RQ_ERR_INVALID_ARG, RQ_ERR_UNSUPPORTED (sizes as above, or 2^31
+ * rows and more), RQ_ERR_CUDA. */
+rq_status rq_paged_cache_init(const rq_paged_config* cfg, void* k_pages, void* v_pages, rq_paged_cache** out);
+
+/* Free the host handle (never the pages).  NULL is ignored. */
+void rq_paged_cache_destroy(rq_paged_cache* cache);
+
+typedef struct {
+  int n_seqs;            /* >= 0 */
+  int n_tokens;          /* rows of the packed tensors */
+  int max_new;           /* no sequence has more new tokens than this */
+  int table_width;       /* entries of a row of page_table, >= 1 */
+  const int* page_table; /* device [n_seqs][table_width] */
+  const int* kv_lens;    /* device [n_seqs] */
+  const int* cu_new;     /* device [n_seqs + 1], or null: one new token each (n_tokens >= n_seqs) */
+} rq_paged_batch;
+
+/* Rotation of queries and keys by position.  Channels are paired j with
+ * j + rot_dim/2, or 2j with 2j + 1 (interleaved); channels from rot_dim on
+ * stay.  Pair j of a token at position p turns by the angle whose cosine and
+ * sine are cos_sin[p][j] and cos_sin[p][rot_dim/2 + j]:
+ *   (a, b) -> (a cos - b sin, b cos + a sin),
+ * products and differences rounded in fp32, the result once to 16 bits.
+ * positions: null = the token's place in its sequence; else device
+ * [n_axes][n_tokens], and the pairs are divided in order among the axes,
+ * sections[a] of them turning by the position on axis a. */
+typedef struct {
+  const float* cos_sin; /* device [n_positions][rot_dim] */
+  int n_positions;      /* >= 1 */
+  int rot_dim;          /* multiple of 16, at most head_dim */
+  int interleaved;
+  const int* positions;
+  int n_axes;           /* 1 to 4; 1 when positions is null */
+  int sections[4];      /* sum over the axes = rot_dim / 2 */
+} rq_rotation;
+
+/* rq_paged_append -- write the batch's new keys and values into one layer's
+ *   pages, keys rotated on the way, and rotate the queries.
+ * k_new, v_new [n_tokens][n_kv_heads][head_dim], q [n_tokens][n_q_heads]
+ *   [head_dim]: a token's heads are contiguous, tokens lie *_stride elements
+ *   apart (a multiple of 8; parts of one fused projection need no copy).
+ * q: nullable.  q_out: contiguous, written for every token of a sequence; may
+ *   be q itself when q is contiguous.  rot: null = no rotation (q must be
+ *   null too).
+ * dev_status: nullable device word for RQ_ERR_DEVICE_INDEX (never cleared here).
+ * A query whose position is outside the table of angles becomes zero.
+ * Errors: RQ_ERR_INVALID_ARG, RQ_ERR_UNSUPPORTED, RQ_ERR_CUDA. */
+rq_status rq_paged_append(rq_paged_cache* cache, int layer, const rq_paged_batch* batch, const rq_rotation* rot,
+                          const void* k_new, int64_t k_stride, const void* v_new, int64_t v_stride, const void* q,
+                          int64_t q_stride, void* q_out, int* dev_status, cudaStream_t stream);
+
+/* Workspace of the attention calls: status word (rq_decode_read_status),
+ * counters, partial results.  Enough for every batch of at most n_seqs
+ * sequences and n_tokens packed tokens, any lengths and prefix; zero it once
+ * with rq_decode_workspace_init.  Calls that share a workspace must not
+ * overlap on the GPU (graphs captured with it among them). */
+rq_status rq_paged_workspace_bytes(const rq_paged_cache* cache, int n_seqs, int n_tokens, size_t* bytes);
+
+/* rq_paged_attention -- attention of the batch's new tokens over the pages of
+ *   one layer, which hold their keys already.  Query i of sequence b stands
+ *   at p = kv_lens[b] - n_b + i and sees key j when
+ *     j <= p and (window == 0 or p - j < window or j < n_sink).
+ *   out = sum_j exp(s q.k_j) v_j / sum_j exp(s q.k_j), accumulated in fp32
+ *   and rounded once; 0 for a query that sees nothing.  Query head h reads kv
+ *   head h / G.  What lies in the pages at tokens that no query of the
+ *   sequence sees (behind its end, before its window) does not matter, NaN
+ *   included.
+ * q: [n_tokens][n_q_heads][head_dim], tokens q_stride elements apart.  out:
+ *   contiguous, same type.  lse: nullable fp32 [n_tokens][n_q_heads], the
+ *   natural logarithm of the denominator (-inf where nothing is seen), with
+ *   which results over parts of the keys can be merged.
+ * softmax_scale <= 0 selects 1/sqrt(head_dim).
+ * Errors: RQ_ERR_INVALID_ARG, RQ_ERR_WORKSPACE, RQ_ERR_CUDA. */
+rq_status rq_paged_attention(rq_paged_cache* cache, int layer, const rq_paged_batch* batch, const void* q,
+                             int64_t q_stride, void* out, float* lse, float softmax_scale, int window, int n_sink,
+                             void* workspace, size_t ws_bytes, cudaStream_t stream);
+
+/* rq_paged_shared_attention -- the same, for sequences that all begin with
+ *   the prefix_len tokens in prefix_pages (device [ceil(prefix_len /
+ *   page_size)]): the batch's tables and lengths count what follows the
+ *   prefix, positions count from its first token (p = prefix_len + kv_lens[b]
+ *   - n_b + i, window and n_sink likewise).  The prefix is read once for the
+ *   queries of the whole batch.
+ * Errors: as rq_paged_attention. */
+rq_status rq_paged_shared_attention(rq_paged_cache* cache, int layer, const rq_paged_batch* batch,
+                                    const int* prefix_pages, int prefix_len, const void* q, int64_t q_stride,
+                                    void* out, float* lse, float softmax_scale, int window, int n_sink,
+                                    void* workspace, size_t ws_bytes, cudaStream_t stream);
 
 /* Name of the last CUDA error a call of this thread reported as RQ_ERR_CUDA
  * ("no error" if none).  Static string, never NULL. */

@@ -21,6 +21,7 @@ RQ_STATUS = {
     5: "RQ_ERR_WORKSPACE",
     6: "RQ_ERR_CUDA",
     7: "RQ_ERR_DEVICE_TIMEOUT",
+    8: "RQ_ERR_DEVICE_INDEX",
 }
 
 
@@ -49,9 +50,40 @@ class CacheConfig(ctypes.Structure):
     ]
 
 
+class PagedConfig(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int) for n in (
+        "n_layers", "n_pages", "page_size", "n_q_heads", "n_kv_heads", "head_dim", "dtype")]
+
+
+class PagedBatch(ctypes.Structure):
+    _fields_ = [
+        ("n_seqs", ctypes.c_int),
+        ("n_tokens", ctypes.c_int),
+        ("max_new", ctypes.c_int),
+        ("table_width", ctypes.c_int),
+        ("page_table", ctypes.c_void_p),
+        ("kv_lens", ctypes.c_void_p),
+        ("cu_new", ctypes.c_void_p),
+    ]
+
+
+class Rotation(ctypes.Structure):
+    _fields_ = [
+        ("cos_sin", ctypes.c_void_p),
+        ("n_positions", ctypes.c_int),
+        ("rot_dim", ctypes.c_int),
+        ("interleaved", ctypes.c_int),
+        ("positions", ctypes.c_void_p),
+        ("n_axes", ctypes.c_int),
+        ("sections", ctypes.c_int * 4),
+    ]
+
+
 _P = ctypes.c_void_p
 _I = ctypes.c_int
 _SZ = ctypes.c_size_t
+_L = ctypes.c_int64
+_F = ctypes.c_float
 _DP = ctypes.POINTER(ctypes.c_double)
 _IP = ctypes.POINTER(ctypes.c_int)
 
@@ -79,6 +111,12 @@ SIGNATURES = {
     "rq_selftest_device_timeout": (_I, [_P, _SZ, ctypes.c_ulonglong, _P]),
     "rq_decode_attention_noalloc": (_I, [_P, _I, _P, _P, ctypes.c_float, _I, _P]),
     "rq_decode_noalloc_read_status": (_I, [_IP]),
+    "rq_paged_cache_init": (_I, [ctypes.POINTER(PagedConfig), _P, _P, ctypes.POINTER(_P)]),
+    "rq_paged_cache_destroy": (None, [_P]),
+    "rq_paged_append": (_I, [_P, _I, _P, _P, _P, _L, _P, _L, _P, _L, _P, _P, _P]),
+    "rq_paged_workspace_bytes": (_I, [_P, _I, _I, ctypes.POINTER(_SZ)]),
+    "rq_paged_attention": (_I, [_P, _I, _P, _P, _L, _P, _P, _F, _I, _I, _P, _SZ, _P]),
+    "rq_paged_shared_attention": (_I, [_P, _I, _P, _P, _I, _P, _L, _P, _P, _F, _I, _I, _P, _SZ, _P]),
 }
 
 _lib = None

@@ -10,7 +10,7 @@ import ctypes
 
 import numpy as np
 
-from ._lib import CacheConfig, check, lib
+from ._lib import CacheConfig, PagedBatch, PagedConfig, Rotation, check, lib
 
 
 def _stream_ptr(stream=None, device=None):
@@ -46,6 +46,11 @@ def _check_tensor(name, t, dtype, shape=None, device_type="cuda", align=16):
     if shape is not None and t.shape != tuple(shape):
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
     raise ValueError(f"{name} must start on a {align}-byte boundary (a view at an offset into a larger tensor?)")
+
+
+def _same_device(name, t, device):
+    if t.get_device() != device:
+        raise ValueError(f"{name} must be on the device of the pages")
 
 
 def rq_allocate_bits(w, alpha, beta, avg_bits, allowed):
@@ -279,3 +284,246 @@ class QuantizedKVCache:
         st = ctypes.c_int(0)
         check("rq_decode_read_status", lib().rq_decode_read_status(_dptr(workspace), ctypes.byref(st)))
         return st.value
+
+
+class PagedKVCache:
+    """A cache of 16-bit keys and values in pages, bound to the caller's page
+    tensors (kept alive by this object): k_pages, v_pages, contiguous bf16 or
+    fp16 CUDA tensors [n_layers, n_pages, n_kv_heads, page_size, head_dim].
+
+    A batch is described with every call.  page_table: int32 [n_seqs, width],
+    token t of a sequence lies in row t % page_size of page
+    page_table[sequence, t // page_size].  kv_lens: int32 [n_seqs], tokens of
+    each sequence, new ones included.  cu_new: int32 [n_seqs + 1], where each
+    sequence's new tokens begin among the packed ones; None: one new token
+    each.  All three are CUDA tensors, read when the kernel runs.
+    """
+
+    def __init__(self, k_pages, v_pages, n_q_heads):
+        import torch
+
+        if not isinstance(k_pages, torch.Tensor) or k_pages.dim() != 5:
+            raise ValueError("k_pages must be a tensor [n_layers, n_pages, n_kv_heads, page_size, head_dim]")
+        if k_pages.dtype not in (torch.bfloat16, torch.float16):
+            raise TypeError(f"k_pages must be torch.bfloat16 or torch.float16, got {k_pages.dtype}")
+        _check_tensor("k_pages", k_pages, k_pages.dtype)
+        _check_tensor("v_pages", v_pages, k_pages.dtype, k_pages.shape)
+        _same_device("v_pages", v_pages, k_pages.get_device())
+        self.k_pages, self.v_pages = k_pages, v_pages
+        self.n_layers, self.n_pages, self.n_kv_heads, self.page_size, self.head_dim = k_pages.shape
+        self.n_q_heads = int(n_q_heads)
+        self.dtype = k_pages.dtype
+        self.device = k_pages.get_device()
+        cfg = PagedConfig(self.n_layers, self.n_pages, self.page_size, self.n_q_heads, self.n_kv_heads,
+                          self.head_dim, 0 if self.dtype is torch.bfloat16 else 1)
+        handle = ctypes.c_void_p(0)
+        with torch.cuda.device(self.device):
+            check("rq_paged_cache_init", lib().rq_paged_cache_init(
+                ctypes.byref(cfg), _dptr(k_pages), _dptr(v_pages), ctypes.byref(handle)))
+            # RQ_ERR_DEVICE_INDEX of the appends (attention calls report in their workspace)
+            self.append_status = torch.zeros(1, dtype=torch.int32, device=k_pages.device)
+        self.handle = handle
+        self._destroy = lib().rq_paged_cache_destroy
+
+    def __del__(self):
+        h = getattr(self, "handle", None)
+        destroy = getattr(self, "_destroy", None)
+        if h is not None and h.value and destroy is not None:
+            destroy(h)
+            self.handle = None
+
+    # -- arguments -----------------------------------------------------------
+    def _batch(self, n_tokens, page_table, kv_lens, cu_new, max_new):
+        import torch
+
+        if not isinstance(page_table, torch.Tensor) or page_table.dim() != 2 or page_table.shape[1] < 1:
+            raise ValueError("page_table must be a tensor [n_seqs, width], width >= 1")
+        n_seqs, width = page_table.shape
+        _check_tensor("page_table", page_table, torch.int32, align=4)
+        _check_tensor("kv_lens", kv_lens, torch.int32, (n_seqs,), align=4)
+        _same_device("page_table", page_table, self.device)
+        _same_device("kv_lens", kv_lens, self.device)
+        if cu_new is None:
+            if n_tokens < n_seqs:
+                raise ValueError(f"{n_tokens} packed tokens for {n_seqs} sequences of one new token each")
+            cu, max_new = None, 1
+        else:
+            _check_tensor("cu_new", cu_new, torch.int32, (n_seqs + 1,), align=4)
+            _same_device("cu_new", cu_new, self.device)
+            cu = cu_new.data_ptr()
+            max_new = n_tokens if max_new is None else int(max_new)
+        return PagedBatch(n_seqs, n_tokens, max_new, width, page_table.data_ptr(), kv_lens.data_ptr(), cu)
+
+    def _packed(self, name, t, heads):
+        """Tokens of `heads` contiguous heads each; the tokens may lie apart
+        (a part of a wider tensor).  Returns the elements between tokens."""
+        import torch
+
+        d = self.head_dim
+        if not isinstance(t, torch.Tensor):
+            raise TypeError(f"{name} must be a torch.Tensor")
+        if t.dtype is not self.dtype:
+            raise TypeError(f"{name} must be {self.dtype}, got {t.dtype}")
+        if t.get_device() != self.device:
+            raise ValueError(f"{name} must be on the device of the pages")
+        if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != d:
+            raise ValueError(f"{name} has shape {tuple(t.shape)}, expected (tokens, {heads}, {d})")
+        s0, s1, s2 = t.stride()
+        if t.shape[0] <= 1:
+            s0 = heads * d
+        if s2 != 1 or (s1 != d and heads > 1) or s0 < heads * d or s0 % 8:
+            raise ValueError(f"{name}: a token's heads must be contiguous and tokens lie a multiple of 8 elements apart")
+        if t.data_ptr() % 16:
+            raise ValueError(f"{name} must start on a 16-byte boundary (a view at an offset into a larger tensor?)")
+        return s0
+
+    def _launch(self, func, stream, *args):
+        """Calls func on `stream` (default: the current stream of the pages'
+        device), with that device current."""
+        import torch
+
+        if stream is None and torch.cuda.current_device() == self.device:
+            check(func, getattr(lib(), func)(*args, torch._C._cuda_getCurrentRawStream(self.device)))
+            return
+        with torch.cuda.device(self.device):
+            check(func, getattr(lib(), func)(*args, _stream_ptr(stream, self.device)))
+
+    # -- calls ---------------------------------------------------------------
+    def rq_paged_append(self, layer, k_new, v_new, page_table, kv_lens, cu_new=None, q=None, q_out=None, cos_sin=None,
+                        positions=None, sections=None, interleaved=False, stream=None):
+        """Write the batch's new keys and values [tokens, n_kv_heads, head_dim]
+        into the layer's pages.  With cos_sin (fp32 [n_positions, rot_dim]:
+        rot_dim/2 cosines, then as many sines, of each position) the keys are
+        rotated on the way and q [tokens, n_q_heads, head_dim], if given, is
+        rotated into q_out (default: a new tensor), which is returned.
+        positions: int32 [tokens], or [axes, tokens] with `sections`, how many
+        channel pairs turn by each axis; None: a token's place in its
+        sequence.  interleaved: channels 2j, 2j + 1 are a pair (else j and
+        j + rot_dim/2)."""
+        import torch
+
+        ks = self._packed("k_new", k_new, self.n_kv_heads)
+        vs = self._packed("v_new", v_new, self.n_kv_heads)
+        n = k_new.shape[0]
+        if v_new.shape[0] != n:
+            raise ValueError(f"v_new has {v_new.shape[0]} tokens, k_new {n}")
+        batch = self._batch(n, page_table, kv_lens, cu_new, None)
+        rot, qs, q_ptr, out_ptr = None, 0, None, None
+        if cos_sin is None:
+            if q is not None or positions is not None or sections is not None:
+                raise ValueError("q, positions and sections go with cos_sin")
+        else:
+            if not isinstance(cos_sin, torch.Tensor) or cos_sin.dim() != 2:
+                raise ValueError("cos_sin must be a tensor [n_positions, rot_dim]")
+            _check_tensor("cos_sin", cos_sin, torch.float32)
+            _same_device("cos_sin", cos_sin, self.device)
+            n_pos, rot_dim = cos_sin.shape
+            pos_ptr, axes = None, 1
+            if positions is not None:
+                axes = positions.shape[0] if positions.dim() == 2 else 1
+                _check_tensor("positions", positions, torch.int32, (axes, n) if positions.dim() == 2 else (n,), align=4)
+                _same_device("positions", positions, self.device)
+                pos_ptr = positions.data_ptr()
+            if not 1 <= axes <= 4:
+                raise ValueError(f"positions on {axes} axes: 1 to 4 are supported")
+            if sections is None:
+                if axes != 1:
+                    raise ValueError("positions on several axes need sections")
+                sections = (rot_dim // 2,)
+            if len(sections) != axes:
+                raise ValueError(f"{len(sections)} sections for positions on {axes} axes")
+            rot = Rotation(cos_sin.data_ptr(), n_pos, rot_dim, int(bool(interleaved)), pos_ptr, axes,
+                           (ctypes.c_int * 4)(*sections))
+            if q is not None:
+                qs = self._packed("q", q, self.n_q_heads)
+                if q.shape[0] != n:
+                    raise ValueError(f"q has {q.shape[0]} tokens, k_new {n}")
+                if q_out is None:
+                    q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+                else:
+                    _check_tensor("q_out", q_out, self.dtype, q.shape)
+                    _same_device("q_out", q_out, self.device)
+                q_ptr, out_ptr = q.data_ptr(), q_out.data_ptr()
+        self._launch("rq_paged_append", stream, self.handle, layer, ctypes.byref(batch),
+                     ctypes.byref(rot) if rot is not None else None, k_new.data_ptr(), ks, v_new.data_ptr(), vs,
+                     q_ptr, qs, out_ptr, self.append_status.data_ptr())
+        return q_out
+
+    def rq_paged_workspace_bytes(self, n_seqs, n_tokens) -> int:
+        out = ctypes.c_size_t(0)
+        check("rq_paged_workspace_bytes", lib().rq_paged_workspace_bytes(self.handle, n_seqs, n_tokens,
+                                                                         ctypes.byref(out)))
+        return out.value
+
+    def make_workspace(self, n_seqs, n_tokens, stream=None):
+        """Workspace for every attention call of at most n_seqs sequences and
+        n_tokens packed tokens.  Calls that share one must not overlap."""
+        import torch
+
+        nb = self.rq_paged_workspace_bytes(n_seqs, n_tokens)
+        ws = torch.empty(nb, dtype=torch.uint8, device=self.k_pages.device)
+        self._launch("rq_decode_workspace_init", stream, _dptr(ws), nb)
+        return ws
+
+    def rq_paged_attention(self, layer, q, page_table, kv_lens, cu_new=None, max_new=None, window=0, n_sink=0,
+                           softmax_scale=0.0, out=None, lse=None, workspace=None, stream=None):
+        """Causal attention of the batch's new tokens q [tokens, n_q_heads,
+        head_dim] over the pages of one layer, which hold their keys and values
+        already.  max_new: the most new tokens any sequence has (default: all
+        of q's).  window: a query sees the last `window` tokens up to itself
+        and the sequence's first n_sink (0: all tokens).  Returns out, in q's
+        type; rows behind the last sequence are left as they were.  lse: fp32
+        [tokens, n_q_heads], filled with the natural logarithm of each
+        softmax's denominator."""
+        return self._attention("rq_paged_attention", (), layer, q, page_table, kv_lens, cu_new, max_new, window,
+                               n_sink, softmax_scale, out, lse, workspace, stream)
+
+    def rq_paged_shared_attention(self, layer, q, prefix_pages, prefix_len, page_table, kv_lens, cu_new=None,
+                                  max_new=None, window=0, n_sink=0, softmax_scale=0.0, out=None, lse=None,
+                                  workspace=None, stream=None):
+        """rq_paged_attention of sequences that all begin with the prefix_len
+        tokens in prefix_pages (int32 [ceil(prefix_len / page_size)]), which
+        are read once for the whole batch; page_table and kv_lens count what
+        follows the prefix, window and n_sink count from its first token."""
+        import torch
+
+        _check_tensor("prefix_pages", prefix_pages, torch.int32, align=4)
+        _same_device("prefix_pages", prefix_pages, self.device)
+        prefix_len = int(prefix_len)
+        if prefix_len < 0 or prefix_pages.numel() * self.page_size < prefix_len:
+            raise ValueError(f"{prefix_pages.numel()} pages of {self.page_size} do not hold {prefix_len} tokens")
+        return self._attention("rq_paged_shared_attention", (prefix_pages.data_ptr(), prefix_len), layer, q,
+                               page_table, kv_lens, cu_new, max_new, window, n_sink, softmax_scale, out, lse,
+                               workspace, stream)
+
+    def _attention(self, func, prefix, layer, q, page_table, kv_lens, cu_new, max_new, window, n_sink, softmax_scale,
+                   out, lse, workspace, stream):
+        import torch
+
+        qs = self._packed("q", q, self.n_q_heads)
+        n = q.shape[0]
+        batch = self._batch(n, page_table, kv_lens, cu_new, max_new)
+        if out is None:
+            out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        else:
+            _check_tensor("out", out, self.dtype, q.shape)
+            _same_device("out", out, self.device)
+        if lse is not None:
+            _check_tensor("lse", lse, torch.float32, (n, self.n_q_heads), align=4)
+            _same_device("lse", lse, self.device)
+        if workspace is None:
+            workspace = self.make_workspace(batch.n_seqs, n, stream)
+        else:
+            _check_tensor("workspace", workspace, torch.uint8)
+            _same_device("workspace", workspace, self.device)
+        self._launch(func, stream, self.handle, layer, ctypes.byref(batch), *prefix, q.data_ptr(), qs, out.data_ptr(),
+                     None if lse is None else lse.data_ptr(), float(softmax_scale), int(window), int(n_sink),
+                     workspace.data_ptr(), workspace.numel())
+        return out
+
+    def read_status(self, workspace=None) -> int:
+        """Blocking read of the status word of an attention workspace, or
+        (None) of the appends: 0, or RQ_ERR_DEVICE_INDEX / _TIMEOUT."""
+        if workspace is None:
+            return int(self.append_status.item())
+        return QuantizedKVCache.rq_decode_read_status(workspace)

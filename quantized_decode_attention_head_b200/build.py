@@ -6,6 +6,7 @@ Usage: python -m quantized_decode_attention_head_b200.build [--verbose-ptxas]
 from __future__ import annotations
 
 import os
+import re
 import subprocess
 import sys
 from concurrent.futures import ThreadPoolExecutor
@@ -17,7 +18,8 @@ OBJ = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "librq.so")
 # the decode kernel is instantiated once per (head_dim, GQA group) pair in its
 # own translation unit, so the units compile in parallel
-SOURCES = ["rq_alloc.cpp", "rq_host.cpp", "rq_quantize.cu", "rq_decode.cu"] + [
+SOURCES = ["rq_alloc.cpp", "rq_host.cpp", "rq_quantize.cu", "rq_decode.cu", "rq_paged_host.cpp",
+           "rq_paged_append.cu", "rq_paged_attn.cu"] + [
     f"rq_decode_{d}x{g}.cu" for d in (128, 64) for g in (1, 2, 4, 8)]
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 
@@ -37,11 +39,22 @@ def _flags(ptxas_verbose=False):
     return f
 
 
+def _deps(path, seen):
+    """path and the headers of this repository that it includes, all levels."""
+    if path not in seen:
+        seen.append(path)
+        with open(path) as f:
+            for name in re.findall(r'^#include "([^"]+)"', f.read(), re.M):
+                for folder in (CSRC, os.path.join(ROOT, "include")):
+                    if os.path.exists(os.path.join(folder, name)):
+                        _deps(os.path.join(folder, name), seen)
+    return seen
+
+
 def _compile(src, ptxas_verbose):
     obj = os.path.join(OBJ, src + ".o")
     path = os.path.join(CSRC, src)
-    deps = [path] + [os.path.join(CSRC, h) for h in os.listdir(CSRC) if h.endswith((".h", ".cuh"))]
-    deps.append(os.path.join(ROOT, "include", "rq.h"))
+    deps = _deps(path, [])
     if not ptxas_verbose and os.path.exists(obj) and os.path.getmtime(obj) >= max(os.path.getmtime(d) for d in deps):
         return obj, ""
     cmd = [_nvcc(), "-c", path, "-o", obj] + _flags(ptxas_verbose)

@@ -137,9 +137,16 @@ int auto_splits(const rq_cache* c, int streams, int n_tiles, int stage_bytes, in
 
 // The last failing CUDA call of this thread (rq_last_cuda_error).
 thread_local cudaError_t g_last_cuda_error = cudaSuccess;
+}  // namespace
+
+namespace rq {
 void note_cuda_error(cudaError_t e) {
   if (e != cudaSuccess) g_last_cuda_error = e;
 }
+}  // namespace rq
+
+namespace {
+using rq::note_cuda_error;
 
 rq_status cuda_status(cudaError_t e) {
   note_cuda_error(e);
@@ -233,6 +240,7 @@ const char* rq_status_string(rq_status s) {
     case RQ_ERR_WORKSPACE: return "workspace too small";
     case RQ_ERR_CUDA: return "CUDA error";
     case RQ_ERR_DEVICE_TIMEOUT: return "device wait timed out";
+    case RQ_ERR_DEVICE_INDEX: return "page, length or position out of range on the device";
   }
   return "unknown status";
 }
@@ -242,7 +250,8 @@ const char* rq_last_cuda_error(void) {
 }
 
 const char* rq_build_info(void) {
-  return "librq: sm_100a; quantize/pack, append/flush, split-K mma.sync decode with bulk-copy pipeline";
+  return "librq: sm_100a; quantize/pack, append/flush, split-K mma.sync decode with bulk-copy pipeline; "
+         "paged 16-bit cache: rotate-and-append, attention";
 }
 
 rq_status rq_cache_bytes(const rq_cache_config* cfg, size_t* bytes) {

@@ -1,0 +1,85 @@
+// Device helpers of the paged 16-bit cache.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "rq_device.cuh"
+#include "rq_paged.h"
+
+namespace rq {
+
+__device__ __forceinline__ void flag_index(int* status) {
+  if (status) *status = kDeviceIndex;
+}
+
+// 16-bit element types of the pages: conversions to and from fp32.
+struct Bf16 {
+  static __device__ __forceinline__ float2 unpack(uint32_t u) {
+    return make_float2(__uint_as_float(u << 16), __uint_as_float(u & 0xFFFF0000u));
+  }
+  static __device__ __forceinline__ uint32_t pack(float lo, float hi) { return pack_bf16x2(lo, hi); }
+};
+struct Fp16 {
+  static __device__ __forceinline__ float2 unpack(uint32_t u) {
+    return __half22float2(*reinterpret_cast<const __half2*>(&u));
+  }
+  static __device__ __forceinline__ uint32_t pack(float lo, float hi) {
+    const __half2 h = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&h);
+  }
+};
+
+// A sequence of the batch as the device finds it: its packed tokens are
+// [t0, t0 + n), it holds len tokens.  Offsets and lengths out of range are
+// brought back into it (and flagged), so that nothing is read or written
+// outside the caller's tensors.
+struct Seq {
+  int t0, n, len;
+};
+__device__ __forceinline__ Seq load_seq(const PagedBatch& b, int i) {
+  Seq s;
+  const int len = __ldg(b.kv_lens + i);
+  const int64_t cap64 = (int64_t)b.width << b.page_shift;
+  const int cap = cap64 > 0x7FFFFFFF ? 0x7FFFFFFF : (int)cap64;
+  s.len = len < 0 ? 0 : (len > cap ? cap : len);
+  bool bad = s.len != len;
+  if (b.cu) {
+    const int lo = __ldg(b.cu + i), hi = __ldg(b.cu + i + 1);
+    bad |= lo < 0 || hi < lo || hi > b.n_tokens;
+    s.t0 = lo < 0 ? 0 : lo;
+    const int e = hi > b.n_tokens ? b.n_tokens : hi;
+    s.n = e > s.t0 ? e - s.t0 : 0;
+  } else {
+    s.t0 = i;
+    s.n = 1;
+  }
+  if (bad) flag_index(b.status);
+  return s;
+}
+
+// The sequence that packed token t belongs to; -1 behind the last one.
+__device__ __forceinline__ int seq_of(const PagedBatch& b, int t) {
+  if (!b.cu) return t < b.n_seqs ? t : -1;
+  int lo = 0, hi = b.n_seqs;  // first index with cu[index + 1] > t
+  while (lo < hi) {
+    const int mid = (lo + hi) >> 1;
+    if (__ldg(b.cu + mid + 1) > t)
+      hi = mid;
+    else
+      lo = mid + 1;
+  }
+  return lo < b.n_seqs ? lo : -1;
+}
+
+// Row (of the layer's first kv head) where page number `page` begins, or -1
+// when the number is out of range.
+__device__ __forceinline__ int64_t page_row(const PagedBatch& b, int page) {
+  if ((unsigned)page >= (unsigned)b.n_pages) {
+    flag_index(b.status);
+    return -1;
+  }
+  return b.page_base + (((int64_t)page * b.hkv) << b.page_shift);
+}
+
+}  // namespace rq

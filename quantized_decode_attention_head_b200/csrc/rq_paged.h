@@ -1,0 +1,62 @@
+// Internal declarations of the paged 16-bit cache (append with rotation,
+// attention over pages).  Not part of the public C ABI (include/rq.h).
+#pragma once
+
+#include <cstddef>
+#include <cstdint>
+
+#include <cuda_runtime.h>
+
+namespace rq {
+
+void note_cuda_error(cudaError_t e);  // rq_last_cuda_error (rq_host.cpp)
+
+constexpr int kDeviceIndex = 8;  // == RQ_ERR_DEVICE_INDEX
+constexpr int kMaxAxes = 4;
+
+// What every paged kernel needs of a cache's layer and a batch.
+struct PagedBatch {
+  const int* table;    // [n_seqs][width]
+  const int* kv_lens;  // [n_seqs]
+  const int* cu;       // [n_seqs + 1] or null
+  int n_seqs, n_tokens, width;
+  int n_pages, page_shift;  // page_size = 1 << page_shift
+  int hq, hkv, g_shift;     // G = 1 << g_shift
+  int64_t page_base;        // rows before the layer's first page
+  int* status;              // nullable in appends
+};
+
+struct PagedAppendArgs {
+  PagedBatch b;
+  uint16_t* k_pages;
+  uint16_t* v_pages;
+  const uint16_t* k_new;
+  const uint16_t* v_new;
+  const uint16_t* q;
+  uint16_t* q_out;
+  int64_t k_stride, v_stride, q_stride;
+  const float* cos_sin;  // null: no rotation
+  const int* positions;
+  int n_positions, rot, interleaved, n_axes;
+  int sections[kMaxAxes];
+};
+
+struct PagedAttnArgs {
+  PagedBatch b;
+  const uint16_t* k_pages;
+  const uint16_t* v_pages;
+  const uint16_t* q;
+  int64_t q_stride;
+  uint16_t* out;
+  float* lse;             // nullable
+  float scale_log2;       // softmax scale * log2(e)
+  int window;             // 0: none
+  int n_sink;
+  const int* prefix;      // pages of the shared prefix, or null
+  int prefix_len;
+};
+
+cudaError_t launch_paged_append(const PagedAppendArgs& a, int head_dim, int dtype, cudaStream_t s);
+cudaError_t launch_paged_attention(const PagedAttnArgs& a, int head_dim, int dtype, cudaStream_t s);
+
+}  // namespace rq

@@ -1,0 +1,190 @@
+// Host side of the paged 16-bit cache: argument checks, workspace layout and
+// launches.  See include/rq.h for the contract.
+#include <cmath>
+#include <new>
+
+#include <cuda_runtime.h>
+
+#include "rq.h"
+#include "rq_paged.h"
+
+struct rq_paged_cache {
+  rq_paged_config cfg;
+  int page_shift, g_shift;
+  uint16_t *k, *v;
+};
+
+namespace {
+
+bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+int log2_of(int x) {
+  int s = 0;
+  while ((1 << s) < x) ++s;
+  return (1 << s) == x ? s : -1;
+}
+
+rq_status cuda_status(cudaError_t e) {
+  rq::note_cuda_error(e);
+  return e == cudaSuccess ? RQ_OK : RQ_ERR_CUDA;
+}
+
+// Checks what all calls of a batch share and fills the kernels' view of it.
+rq_status fill_batch(const rq_paged_cache* c, int layer, const rq_paged_batch* b, rq::PagedBatch& o) {
+  if (!c || !b || layer < 0 || layer >= c->cfg.n_layers) return RQ_ERR_INVALID_ARG;
+  if (b->n_seqs < 0 || b->n_tokens < 0 || b->max_new < 0 || b->table_width < 1) return RQ_ERR_INVALID_ARG;
+  if (b->n_seqs > 0 && (!b->page_table || !b->kv_lens)) return RQ_ERR_INVALID_ARG;
+  if (!aligned4(b->page_table) || !aligned4(b->kv_lens) || !aligned4(b->cu_new)) return RQ_ERR_INVALID_ARG;
+  if (!b->cu_new && b->n_tokens < b->n_seqs) return RQ_ERR_INVALID_ARG;
+  o.table = b->page_table;
+  o.kv_lens = b->kv_lens;
+  o.cu = b->cu_new;
+  o.n_seqs = b->n_seqs;
+  o.n_tokens = b->n_tokens;
+  o.width = b->table_width;
+  o.n_pages = c->cfg.n_pages;
+  o.page_shift = c->page_shift;
+  o.hq = c->cfg.n_q_heads;
+  o.hkv = c->cfg.n_kv_heads;
+  o.g_shift = c->g_shift;
+  o.page_base = (int64_t)layer * c->cfg.n_pages * c->cfg.n_kv_heads * c->cfg.page_size;
+  return RQ_OK;
+}
+
+bool good_stride(int64_t stride, int heads, int d) { return stride >= (int64_t)heads * d && stride % 8 == 0; }
+
+constexpr size_t kStatusBytes = 256;
+
+rq_status attention(rq_paged_cache* c, int layer, const rq_paged_batch* batch, const int* prefix, int prefix_len,
+                    const void* q, int64_t q_stride, void* out, float* lse, float softmax_scale, int window,
+                    int n_sink, void* workspace, size_t ws_bytes, cudaStream_t stream) {
+  rq::PagedAttnArgs a;
+  const rq_status st = fill_batch(c, layer, batch, a.b);
+  if (st != RQ_OK) return st;
+  if (window < 0 || n_sink < 0 || prefix_len < 0 || !(softmax_scale <= 3.0e38f)) return RQ_ERR_INVALID_ARG;
+  if (prefix_len > 0 && (!prefix || !aligned4(prefix))) return RQ_ERR_INVALID_ARG;
+  if (!workspace || !aligned16(workspace)) return RQ_ERR_INVALID_ARG;
+  if (batch->n_tokens > 0 && (!q || !out || !aligned16(q) || !aligned16(out) || !aligned4(lse) ||
+                              !good_stride(q_stride, c->cfg.n_q_heads, c->cfg.head_dim)))
+    return RQ_ERR_INVALID_ARG;
+  size_t need = 0;
+  if (rq_paged_workspace_bytes(c, batch->n_seqs, batch->n_tokens, &need) != RQ_OK) return RQ_ERR_INVALID_ARG;
+  if (ws_bytes < need) return RQ_ERR_WORKSPACE;
+  if (batch->n_tokens == 0 || batch->n_seqs == 0) return RQ_OK;
+  a.b.status = static_cast<int*>(workspace);
+  a.k_pages = c->k;
+  a.v_pages = c->v;
+  a.q = static_cast<const uint16_t*>(q);
+  a.q_stride = q_stride;
+  a.out = static_cast<uint16_t*>(out);
+  a.lse = lse;
+  const float scale = softmax_scale > 0.0f ? softmax_scale : 1.0f / std::sqrt((float)c->cfg.head_dim);
+  a.scale_log2 = scale * 1.4426950408889634f;
+  a.window = window;
+  a.n_sink = n_sink;
+  a.prefix = prefix_len > 0 ? prefix : nullptr;
+  a.prefix_len = prefix_len;
+  return cuda_status(rq::launch_paged_attention(a, c->cfg.head_dim, c->cfg.dtype, stream));
+}
+
+}  // namespace
+
+extern "C" {
+
+rq_status rq_paged_cache_init(const rq_paged_config* cfg, void* k_pages, void* v_pages, rq_paged_cache** out) {
+  if (!cfg || !k_pages || !v_pages || !out) return RQ_ERR_INVALID_ARG;
+  if (cfg->n_layers < 1 || cfg->n_pages < 1 || cfg->n_q_heads < 1 || cfg->n_kv_heads < 1) return RQ_ERR_INVALID_ARG;
+  if (!aligned16(k_pages) || !aligned16(v_pages)) return RQ_ERR_INVALID_ARG;
+  if (cfg->head_dim != 64 && cfg->head_dim != 128) return RQ_ERR_UNSUPPORTED;
+  if (cfg->page_size != 16 && cfg->page_size != 32 && cfg->page_size != 64 && cfg->page_size != 128)
+    return RQ_ERR_UNSUPPORTED;
+  if (cfg->dtype != 0 && cfg->dtype != 1) return RQ_ERR_UNSUPPORTED;
+  if (cfg->n_q_heads % cfg->n_kv_heads != 0) return RQ_ERR_UNSUPPORTED;
+  const int g = cfg->n_q_heads / cfg->n_kv_heads;
+  if (g != 1 && g != 2 && g != 4 && g != 8) return RQ_ERR_UNSUPPORTED;
+  const double rows = (double)cfg->n_layers * cfg->n_pages * cfg->n_kv_heads * cfg->page_size;
+  if (rows >= 2147483648.0 || cfg->n_kv_heads > 65535) return RQ_ERR_UNSUPPORTED;
+  rq_paged_cache* c = new (std::nothrow) rq_paged_cache();
+  if (!c) return RQ_ERR_INVALID_ARG;
+  c->cfg = *cfg;
+  c->page_shift = log2_of(cfg->page_size);
+  c->g_shift = log2_of(g);
+  c->k = static_cast<uint16_t*>(k_pages);
+  c->v = static_cast<uint16_t*>(v_pages);
+  *out = c;
+  return RQ_OK;
+}
+
+void rq_paged_cache_destroy(rq_paged_cache* cache) { delete cache; }
+
+rq_status rq_paged_append(rq_paged_cache* c, int layer, const rq_paged_batch* batch, const rq_rotation* rot,
+                          const void* k_new, int64_t k_stride, const void* v_new, int64_t v_stride, const void* q,
+                          int64_t q_stride, void* q_out, int* dev_status, cudaStream_t stream) {
+  rq::PagedAppendArgs a = {};
+  const rq_status st = fill_batch(c, layer, batch, a.b);
+  if (st != RQ_OK) return st;
+  if (!aligned4(dev_status) || (q && !rot)) return RQ_ERR_INVALID_ARG;
+  const int d = c->cfg.head_dim;
+  if (batch->n_tokens > 0) {
+    if (!k_new || !v_new || !aligned16(k_new) || !aligned16(v_new)) return RQ_ERR_INVALID_ARG;
+    if (!good_stride(k_stride, c->cfg.n_kv_heads, d) || !good_stride(v_stride, c->cfg.n_kv_heads, d))
+      return RQ_ERR_INVALID_ARG;
+    if (q && (!q_out || !aligned16(q) || !aligned16(q_out) || !good_stride(q_stride, c->cfg.n_q_heads, d)))
+      return RQ_ERR_INVALID_ARG;
+  }
+  if (rot) {
+    if (!rot->cos_sin || !aligned16(rot->cos_sin) || rot->n_positions < 1) return RQ_ERR_INVALID_ARG;
+    if (rot->rot_dim < 16 || rot->rot_dim > d || rot->rot_dim % 16 != 0) return RQ_ERR_UNSUPPORTED;
+    if (rot->n_axes < 1 || rot->n_axes > rq::kMaxAxes) return RQ_ERR_UNSUPPORTED;
+    if (!aligned4(rot->positions) || (!rot->positions && rot->n_axes != 1)) return RQ_ERR_INVALID_ARG;
+    int64_t sum = 0;
+    for (int k = 0; k < rot->n_axes; ++k) {
+      if (rot->sections[k] < 0) return RQ_ERR_INVALID_ARG;
+      sum += rot->sections[k];
+      a.sections[k] = rot->sections[k];
+    }
+    if (sum != rot->rot_dim / 2) return RQ_ERR_INVALID_ARG;
+    a.cos_sin = rot->cos_sin;
+    a.positions = rot->positions;
+    a.n_positions = rot->n_positions;
+    a.rot = rot->rot_dim;
+    a.interleaved = rot->interleaved ? 1 : 0;
+    a.n_axes = rot->n_axes;
+  }
+  if (batch->n_tokens == 0 || batch->n_seqs == 0) return RQ_OK;
+  a.b.status = dev_status;
+  a.k_pages = c->k;
+  a.v_pages = c->v;
+  a.k_new = static_cast<const uint16_t*>(k_new);
+  a.v_new = static_cast<const uint16_t*>(v_new);
+  a.q = static_cast<const uint16_t*>(q);
+  a.q_out = static_cast<uint16_t*>(q_out);
+  a.k_stride = k_stride;
+  a.v_stride = v_stride;
+  a.q_stride = q_stride;
+  return cuda_status(rq::launch_paged_append(a, d, c->cfg.dtype, stream));
+}
+
+rq_status rq_paged_workspace_bytes(const rq_paged_cache* c, int n_seqs, int n_tokens, size_t* bytes) {
+  if (!c || !bytes || n_seqs < 0 || n_tokens < 0) return RQ_ERR_INVALID_ARG;
+  *bytes = kStatusBytes;
+  return RQ_OK;
+}
+
+rq_status rq_paged_attention(rq_paged_cache* c, int layer, const rq_paged_batch* batch, const void* q,
+                             int64_t q_stride, void* out, float* lse, float softmax_scale, int window, int n_sink,
+                             void* workspace, size_t ws_bytes, cudaStream_t stream) {
+  return attention(c, layer, batch, nullptr, 0, q, q_stride, out, lse, softmax_scale, window, n_sink, workspace,
+                   ws_bytes, stream);
+}
+
+rq_status rq_paged_shared_attention(rq_paged_cache* c, int layer, const rq_paged_batch* batch,
+                                    const int* prefix_pages, int prefix_len, const void* q, int64_t q_stride,
+                                    void* out, float* lse, float softmax_scale, int window, int n_sink,
+                                    void* workspace, size_t ws_bytes, cudaStream_t stream) {
+  return attention(c, layer, batch, prefix_pages, prefix_len, q, q_stride, out, lse, softmax_scale, window, n_sink,
+                   workspace, ws_bytes, stream);
+}
+
+}  // extern "C"
