@@ -19,6 +19,9 @@ struct Bf16 {
     return make_float2(__uint_as_float(u << 16), __uint_as_float(u & 0xFFFF0000u));
   }
   static __device__ __forceinline__ uint32_t pack(float lo, float hi) { return pack_bf16x2(lo, hi); }
+  static __device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    mma_bf16_k16(d, a[0], a[1], a[2], a[3], b0, b1);
+  }
 };
 struct Fp16 {
   static __device__ __forceinline__ float2 unpack(uint32_t u) {
@@ -27,6 +30,13 @@ struct Fp16 {
   static __device__ __forceinline__ uint32_t pack(float lo, float hi) {
     const __half2 h = __floats2half2_rn(lo, hi);
     return *reinterpret_cast<const uint32_t*>(&h);
+  }
+  static __device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 "
+        "{%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};\n"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
   }
 };
 
@@ -80,6 +90,24 @@ __device__ __forceinline__ int64_t page_row(const PagedBatch& b, int page) {
     return -1;
   }
   return b.page_base + (((int64_t)page * b.hkv) << b.page_shift);
+}
+
+// Four channels of a row's state (v not yet divided by l, maximum m in log2
+// units): the result, or the row's partial state for the merge of the parts.
+template <class T, int D>
+__device__ __forceinline__ void store_row(const PagedAttnArgs& a, int token, int head, int c4, float4 v, float m,
+                                          float l) {
+  const int64_t row = (int64_t)token * a.b.hq + head;
+  if (a.rows_o) {
+    const int64_t at = (int64_t)a.row_slot * a.b.n_tokens * a.b.hq + row;
+    *reinterpret_cast<float4*>(a.rows_o + at * D + 4 * c4) = v;
+    if (c4 == 0) *reinterpret_cast<float2*>(a.rows_ml + 2 * at) = make_float2(m, l);
+    return;
+  }
+  const float inv = l == 0.f ? 0.f : 1.f / l;
+  *reinterpret_cast<uint2*>(a.out + row * D + 4 * c4) =
+      make_uint2(T::pack(v.x * inv, v.y * inv), T::pack(v.z * inv, v.w * inv));
+  if (c4 == 0 && a.lse) a.lse[row] = l == 0.f ? -INFINITY : m * 0.6931471805599453f + logf(l);
 }
 
 }  // namespace rq

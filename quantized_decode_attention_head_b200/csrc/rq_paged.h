@@ -5,6 +5,7 @@
 #include <cstddef>
 #include <cstdint>
 
+#include <cuda.h>
 #include <cuda_runtime.h>
 
 namespace rq {
@@ -54,9 +55,24 @@ struct PagedAttnArgs {
   int n_sink;
   const int* prefix;      // pages of the shared prefix, or null
   int prefix_len;
+  int few_rows_only;      // the call said that no sequence has more than 16 rows a kv head
+  int n_ctas;             // CTAs of the decode kernel, at most kMaxParts
+  float* parts;           // its partial states: two slots of part_floats(D) a CTA
+  uint32_t* counters;     // one a CTA: parts of the stream that begins to be split there
+  float* rows_o;          // null: results go to out; else partial states of whole rows,
+  float* rows_ml;         //   [row_slot][n_tokens][hq][D] and [..][2] (maximum in log2 units, sum)
+  int row_slot;
 };
 
+// Most CTAs among which one stream of the decode kernel can be split.
+constexpr int kMaxParts = 160;
+constexpr int kDecodeRows = 16;  // rows of a kv head that the decode kernel takes
+// o[16][D], then (m, l) of each row
+__host__ __device__ constexpr int part_floats(int D) { return kDecodeRows * D + 2 * kDecodeRows; }
+
 cudaError_t launch_paged_append(const PagedAppendArgs& a, int head_dim, int dtype, cudaStream_t s);
+cudaError_t launch_paged_decode(const CUtensorMap& km, const CUtensorMap& vm, const PagedAttnArgs& a, int head_dim,
+                                int dtype, cudaStream_t s);
 cudaError_t launch_paged_attention(const PagedAttnArgs& a, int head_dim, int dtype, cudaStream_t s);
 
 }  // namespace rq

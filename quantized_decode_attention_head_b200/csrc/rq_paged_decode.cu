@@ -1,0 +1,511 @@
+// Attention of few query rows per sequence over the paged 16-bit cache
+// (sm_100a): single tokens and short drafts, n_b * G <= 16 rows a kv head.
+//
+// Memory bound: every visible key and value row is read once for the G query
+// heads (and drafted tokens) that share it, 4 G flops for 4 bytes.  So the
+// design is a stream: each warp owns a ring of stages, 32 tokens of keys and
+// values each, that its first lane keeps filling with tiled TMA copies (one
+// box per page and 64 channels, 128-byte swizzle, so that the ldmatrix reads
+// are free of bank conflicts); 192 KB an SM are in flight at head_dim 128.
+//
+// Work is split over the tokens, whatever the lengths: the visible tokens of
+// all (sequence, kv head) streams, in units of 128, form one line that the
+// CTAs (one per SM) divide evenly.  The line is laid out on the device from
+// the lengths, so a captured launch follows them.  A CTA whose share ends
+// inside a stream publishes a partial softmax state (at most two a CTA: its
+// first and its last stream); the last of a stream's CTAs to arrive merges
+// them in the order of the CTAs, so results do not depend on timing.
+//
+// Products run on mma.sync m16n8k16 (rows = token, head), fp32 accumulation;
+// the weights enter the second product as two 16-bit terms (high and rest,
+// 2^-16 relative or better), which costs tensor issue slots that a stream of
+// memory leaves idle and keeps their rounding out of the result.
+#include <cuda.h>
+
+#include "rq_paged.cuh"
+
+namespace rq {
+namespace {
+
+constexpr int NW = 4;         // warps a CTA
+constexpr int kChunk = 32;    // tokens a stage
+constexpr int kRows = 16;     // query rows of an MMA
+
+template <int D>
+struct Cfg {
+  static constexpr int P = D / 64;                      // 64-channel panels of a row
+  static constexpr int PANEL = kChunk * 128;            // bytes of a panel of a stage
+  static constexpr int HALF = P * PANEL;                // keys or values of a stage
+  static constexpr int STAGE = 2 * HALF;
+  static constexpr int S = 3 * 16384 / STAGE;           // stages a warp: 48 KB
+  static constexpr int RING = NW * S * STAGE;
+  static constexpr int OSTR = D + 4;                    // floats of a row of the merge buffer
+  static constexpr int MERGE = NW * kRows * OSTR * 4;
+  static constexpr int SMEM = 1024 + RING + MERGE;      // ring aligned to 1024 bytes
+};
+
+// One sequence as the kernel walks it: the 32-token chunks that any of its
+// queries sees are, in order, chunks [0, ns) (first tokens) and [lo_c, ...).
+struct Walk {
+  int t0, n, len;      // packed tokens, tokens held
+  int lo, sink;        // tokens [0, sink) and [lo, len) are seen by some query
+  int ns, lo_c, chunks, units;
+};
+__device__ __forceinline__ Walk walk_of(const PagedAttnArgs& a, int b) {
+  Walk w;
+  const Seq s = load_seq(a.b, b);
+  w.t0 = s.t0;
+  w.n = s.n;
+  w.len = s.len;
+  const int first = a.prefix_len + s.len - s.n;  // position of the first query
+  int lo = a.window > 0 ? first + 1 - a.window - a.prefix_len : 0;
+  lo = lo < 0 ? 0 : (lo > s.len ? s.len : lo);
+  int sink = a.window > 0 ? a.n_sink - a.prefix_len : 0;
+  sink = sink < 0 ? 0 : (sink > s.len ? s.len : sink);
+  w.lo = lo;
+  w.sink = sink;
+  w.lo_c = lo / kChunk;
+  const int sc = (sink + kChunk - 1) / kChunk;
+  w.ns = sc < w.lo_c ? sc : w.lo_c;
+  w.chunks = w.ns + (s.len + kChunk - 1) / kChunk - w.lo_c;
+  const bool mine = s.n > 0 && (s.n << a.b.g_shift) <= kRows;
+  if (s.n > 0 && !mine && a.few_rows_only) flag_index(a.b.status);  // more new tokens than max_new said
+  w.units = mine ? (w.chunks > NW ? (w.chunks + NW - 1) / NW : 1) : 0;  // a stream that sees nothing still writes
+  return w;
+}
+
+// A place on the line of units: unit i of kv head h of sequence b.
+struct Cursor {
+  Walk w;
+  int b, h, i;
+  __device__ __forceinline__ void next(const PagedAttnArgs& a) {
+    if (++i < w.units) return;
+    i = 0;
+    if (++h < a.b.hkv) return;
+    h = 0;
+    do {
+      ++b;
+      w.units = 0;
+      if (b < a.b.n_seqs) w = walk_of(a, b);
+    } while (b < a.b.n_seqs && w.units == 0);
+  }
+};
+
+__device__ __forceinline__ int chunk_token(const Walk& w, int c) {
+  return kChunk * (c < w.ns ? c : w.lo_c + c - w.ns);
+}
+
+__device__ __forceinline__ void tma_box(uint32_t dst, const CUtensorMap* map, int x, int y, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];\n" ::"r"(
+          dst),
+      "l"(map), "r"(x), "r"(y), "r"(smem_u32(bar))
+      : "memory");
+}
+
+// First unit of CTA c when U units are divided among n CTAs (n <= U).
+__device__ __forceinline__ int64_t share_begin(int64_t c, int64_t U, int64_t n) { return c * U / n; }
+// The CTA whose share holds unit u.
+__device__ __forceinline__ int share_of(int64_t u, int64_t U, int64_t n) { return (int)(((u + 1) * n + U - 1) / U - 1); }
+
+template <class T, int D>
+__global__ void __launch_bounds__(NW * 32, 1)
+    paged_decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
+                        const __grid_constant__ PagedAttnArgs a) {
+  using C = Cfg<D>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  float* merge = reinterpret_cast<float*>(ring + C::RING);
+  __shared__ uint64_t full[NW][C::S];
+  __shared__ uint32_t pages_ok[NW][C::S];  // bit k: the page of tokens 16 k.. of the chunk exists
+  __shared__ float ml[NW][kRows][2];
+  __shared__ int64_t sh64[NW + 2];
+  __shared__ int sh32[2];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int gid = lane >> 2, tig = lane & 3;
+
+  // ---- the line of units: its length, and where this CTA's share begins
+  int64_t mine = 0;
+  for (int b = tid; b < a.b.n_seqs; b += NW * 32) mine += walk_of(a, b).units;
+#pragma unroll
+  for (int k = 16; k; k >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, k);
+  if (lane == 0) sh64[warp] = mine;
+  if (tid < NW * C::S) mbar_init(&full[tid / C::S][tid % C::S], 1);
+  mbar_fence_init();
+  __syncthreads();
+  const int64_t U = (sh64[0] + sh64[1] + sh64[2] + sh64[3]) * a.b.hkv;
+  const int64_t N = U < (int64_t)gridDim.x ? U : (int64_t)gridDim.x;
+  const int cta = blockIdx.x;
+  if (cta >= N) return;
+  const int64_t u0 = share_begin(cta, U, N), u1 = share_begin(cta + 1, U, N);
+  __syncthreads();
+  Cursor cur;
+  int64_t base = 0;  // first unit of the current sequence
+  {
+    const int64_t want = u0 / a.b.hkv;  // in units of all heads: sequences take units * hkv each
+    int64_t before = 0;
+    for (int b0 = 0;; b0 += NW * 32) {
+      if (b0 >= a.b.n_seqs) return;  // the lengths changed under the call
+      const int b = b0 + tid;
+      int64_t v = b < a.b.n_seqs ? walk_of(a, b).units : 0, x = v;
+#pragma unroll
+      for (int k = 1; k < 32; k <<= 1) {
+        const int64_t y = __shfl_up_sync(0xffffffffu, x, k);
+        if (lane >= k) x += y;
+      }
+      if (lane == 31) sh64[warp] = x;
+      __syncthreads();
+      int64_t sum = 0;
+#pragma unroll
+      for (int k = 0; k < NW; ++k) {
+        if (k < warp) x += sh64[k];
+        sum += sh64[k];
+      }
+      if (want >= before + x - v && want < before + x) {
+        sh32[0] = b;
+        sh64[NW] = before + x - v;
+      }
+      const bool found = want < before + sum;
+      __syncthreads();
+      if (found) break;
+      before += sum;
+    }
+    cur.b = sh32[0];
+    base = sh64[NW] * a.b.hkv;
+    cur.w = walk_of(a, cur.b);
+    const int64_t rem = u0 - base;
+    cur.h = (int)(rem / cur.w.units);
+    cur.i = (int)(rem % cur.w.units);
+  }
+
+  // ---- the warp's ring: its producer runs ahead on the same line
+  Cursor ahead = cur;
+  int64_t left = u1 - u0;  // units the producer has not passed
+  int put = 0, put_n = 0;  // next slot to fill, chunks issued and not yet consumed
+  const int box = a.b.page_shift < 5 ? 16 : 32;  // tokens of one copy
+  auto produce = [&]() {
+    // issue chunks until the ring is full or the share ends
+    while (left > 0 && put_n < C::S) {
+      const int c = ahead.i * NW + warp;
+      if (c < ahead.w.chunks) {
+        if (lane == 0) {
+          const int t = chunk_token(ahead.w, c);
+          const int* row = a.b.table + (int64_t)ahead.b * a.b.width;
+          uint8_t* st = ring + (warp * C::S + put) * C::STAGE;
+          uint32_t ok = 0;
+          int at[2];
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            at[k] = -1;
+            if (16 * k < kChunk && (k == 0 || box == 16) && t + 16 * k < ahead.w.len) {
+              const int tt = t + 16 * k;
+              const int64_t r = page_row(a.b, __ldg(row + (tt >> a.b.page_shift)));
+              if (r >= 0) {
+                at[k] = (int)r + (ahead.h << a.b.page_shift) + (tt & ((1 << a.b.page_shift) - 1));
+                ok |= box == 32 ? 3u : 1u << k;
+              }
+            }
+          }
+          pages_ok[warp][put] = ok;
+          uint64_t* bar = &full[warp][put];
+          const uint32_t bytes = 2 * C::P * 128 * box * ((at[0] >= 0) + (at[1] >= 0));
+          if (bytes) {
+            mbar_arrive_expect_tx(bar, bytes);
+#pragma unroll
+            for (int k = 0; k < 2; ++k)
+              if (at[k] >= 0) {
+#pragma unroll
+                for (int p = 0; p < C::P; ++p) {
+                  tma_box(smem_u32(st + p * C::PANEL + k * 2048), &kmap, 64 * p, at[k], bar);
+                  tma_box(smem_u32(st + C::HALF + p * C::PANEL + k * 2048), &vmap, 64 * p, at[k], bar);
+                }
+              }
+          } else {
+            mbar_arrive(bar);
+          }
+        }
+        put = put + 1 == C::S ? 0 : put + 1;
+        ++put_n;
+      }
+      ahead.next(a);
+      --left;
+    }
+  };
+  produce();
+
+  int get = 0;
+  uint32_t phase = 0;
+  bool dead = false;  // a wait gave up
+  const int G = 1 << a.b.g_shift;
+  int64_t u = u0;
+  while (u < u1 && cur.b < a.b.n_seqs) {
+    // ---- one stream's part of the share: units [cur.i, i_end) of (b, h)
+    const Walk w = cur.w;
+    const int h = cur.h, i_begin = cur.i;
+    const int64_t stream = base + (int64_t)h * w.units;  // its first unit
+    const int i_end = (int)(w.units < i_begin + (u1 - u) ? w.units : i_begin + (u1 - u));
+    const int R = w.n << a.b.g_shift;
+
+    uint32_t qf[D / 16][4];
+#pragma unroll
+    for (int rr = 0; rr < 2; ++rr) {
+      const int r = gid + 8 * rr;
+      const uint16_t* qp = a.q + (w.t0 + (r >> a.b.g_shift)) * a.q_stride + (h * G + (r & (G - 1))) * D + 2 * tig;
+#pragma unroll
+      for (int ks = 0; ks < D / 16; ++ks) {
+        qf[ks][rr] = r < R ? __ldg(reinterpret_cast<const uint32_t*>(qp + 16 * ks)) : 0u;
+        qf[ks][2 + rr] = r < R ? __ldg(reinterpret_cast<const uint32_t*>(qp + 16 * ks + 8)) : 0u;
+      }
+    }
+    float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+    float o[D / 8][4];
+#pragma unroll
+    for (int c = 0; c < D / 8; ++c)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) o[c][e] = 0.f;
+    const int p_first = w.len - w.n;  // local positions (the prefix left out)
+    const int p_row[2] = {p_first + (gid >> a.b.g_shift), p_first + ((gid + 8) >> a.b.g_shift)};
+
+    for (int i = i_begin; i < i_end; ++i) {
+      const int c = i * NW + warp;
+      if (c >= w.chunks) break;
+      const int t = chunk_token(w, c);
+      if (!dead && !mbar_wait_bounded(&full[warp][get], phase)) {
+        dead = true;
+        if (lane == 0) *a.b.status = kDeviceTimeout;
+      }
+      __syncwarp();
+      uint8_t* st = ring + (warp * C::S + get) * C::STAGE;
+      const uint32_t kb = smem_u32(st), vb = smem_u32(st + C::HALF);
+      // tokens that some query sees; the values of the others are made zero,
+      // since 0 * NaN would reach the sum
+      const int j = t + lane;
+      const bool live = j < w.len && (j >= w.lo || j < w.sink) && ((pages_ok[warp][get] >> (lane >> 4)) & 1u);
+      const uint32_t lives = __ballot_sync(0xffffffffu, live);
+      if (lives != 0xffffffffu) {
+        if (!live) {
+#pragma unroll
+          for (int p = 0; p < C::P; ++p)
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+              *reinterpret_cast<uint4*>(st + C::HALF + p * C::PANEL + lane * 128 + e * 16) = make_uint4(0, 0, 0, 0);
+        }
+        fence_proxy_async_smem();  // before a later copy into this slot
+        __syncwarp();
+      }
+      float s[4][4];
+#pragma unroll
+      for (int nb = 0; nb < 4; ++nb)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) s[nb][e] = 0.f;
+      const int mi = lane >> 3, mr = lane & 7;
+#pragma unroll
+      for (int ks = 0; ks < D / 16; ++ks) {
+        const int c16 = (ks & 3) * 2 + (mi & 1);
+#pragma unroll
+        for (int np = 0; np < 2; ++np) {
+          const int tok = np * 16 + (mi >> 1) * 8 + mr;
+          uint32_t kf[4];
+          ldsm_x4(kf, kb + (ks >> 2) * C::PANEL + tok * 128 + ((c16 ^ mr) << 4));
+          T::mma(s[2 * np], qf[ks], kf[0], kf[1]);
+          T::mma(s[2 * np + 1], qf[ks], kf[2], kf[3]);
+        }
+      }
+      const bool whole = lives == 0xffffffffu && t + kChunk - 1 <= p_first &&
+                         (a.window == 0 || t > p_first + w.n - 1 - a.window || t + kChunk <= w.sink);
+      if (!whole) {
+#pragma unroll
+        for (int nb = 0; nb < 4; ++nb)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int col = nb * 8 + 2 * tig + (e & 1), jj = t + col, p = p_row[e >> 1];
+            const bool see = ((lives >> col) & 1u) && jj <= p && (a.window == 0 || p - jj < a.window || jj < w.sink);
+            if (!see) s[nb][e] = -INFINITY;
+          }
+      }
+#pragma unroll
+      for (int rr = 0; rr < 2; ++rr) {
+        float mx = -INFINITY;
+#pragma unroll
+        for (int nb = 0; nb < 4; ++nb) mx = fmaxf(mx, fmaxf(s[nb][2 * rr], s[nb][2 * rr + 1]));
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+        const float mn = fmaxf(m[rr], mx * a.scale_log2);
+        const float mu = mn == -INFINITY ? 0.f : mn;  // nothing seen yet: weights become 0
+        const float alpha = ex2(m[rr] - mu);
+        m[rr] = mn;
+        float sum = 0.f;
+#pragma unroll
+        for (int nb = 0; nb < 4; ++nb)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const float pr = ex2(fmaf(s[nb][2 * rr + e], a.scale_log2, -mu));
+            s[nb][2 * rr + e] = pr;
+            sum += pr;
+          }
+        l[rr] = fmaf(l[rr], alpha, sum);
+#pragma unroll
+        for (int cc = 0; cc < D / 8; ++cc) {
+          o[cc][2 * rr] *= alpha;
+          o[cc][2 * rr + 1] *= alpha;
+        }
+      }
+#pragma unroll
+      for (int kt = 0; kt < 2; ++kt) {
+        uint32_t hi[4], lo[4];
+#pragma unroll
+        for (int f = 0; f < 4; ++f) {
+          const float x = s[2 * kt + (f >> 1)][2 * (f & 1)], y = s[2 * kt + (f >> 1)][2 * (f & 1) + 1];
+          hi[f] = T::pack(x, y);
+          const float2 r = T::unpack(hi[f]);
+          lo[f] = T::pack(x - r.x, y - r.y);
+        }
+#pragma unroll
+        for (int cp = 0; cp < D / 16; ++cp) {
+          const int tok = kt * 16 + (mi & 1) * 8 + mr, c16 = (cp & 3) * 2 + (mi >> 1);
+          uint32_t vf[4];
+          ldsm_x4_trans(vf, vb + (cp >> 2) * C::PANEL + tok * 128 + ((c16 ^ mr) << 4));
+          T::mma(o[2 * cp], hi, vf[0], vf[1]);
+          T::mma(o[2 * cp + 1], hi, vf[2], vf[3]);
+          T::mma(o[2 * cp], lo, vf[0], vf[1]);
+          T::mma(o[2 * cp + 1], lo, vf[2], vf[3]);
+        }
+      }
+      __syncwarp();  // every lane has read the slot
+      if (++get == C::S) {
+        get = 0;
+        phase ^= 1;
+      }
+      --put_n;
+      produce();
+    }
+
+    // ---- merge the four warps
+#pragma unroll
+    for (int rr = 0; rr < 2; ++rr) {
+      l[rr] += __shfl_xor_sync(0xffffffffu, l[rr], 1);
+      l[rr] += __shfl_xor_sync(0xffffffffu, l[rr], 2);
+      const int r = gid + 8 * rr;
+      if (r < R) {
+        if (tig == 0) {
+          ml[warp][r][0] = m[rr];
+          ml[warp][r][1] = l[rr];
+        }
+#pragma unroll
+        for (int cc = 0; cc < D / 8; ++cc)
+          *reinterpret_cast<float2*>(merge + (warp * kRows + r) * C::OSTR + 8 * cc + 2 * tig) =
+              make_float2(o[cc][2 * rr], o[cc][2 * rr + 1]);
+      }
+    }
+    __syncthreads();
+    const bool all = i_begin == 0 && i_end == w.units;
+    float* part = a.parts + (int64_t)(2 * cta + (u == u0 ? 0 : 1)) * part_floats(D);
+    for (int it = tid; it < R * (D / 4); it += NW * 32) {
+      const int r = it / (D / 4), c4 = it % (D / 4);
+      float M = -INFINITY;
+#pragma unroll
+      for (int k = 0; k < NW; ++k) M = fmaxf(M, ml[k][r][0]);
+      const float mu = M == -INFINITY ? 0.f : M;
+      float L = 0.f;
+      float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int k = 0; k < NW; ++k) {
+        const float f = ex2(ml[k][r][0] - mu);
+        const float4 x = *reinterpret_cast<const float4*>(merge + (k * kRows + r) * C::OSTR + 4 * c4);
+        L = fmaf(f, ml[k][r][1], L);
+        v.x = fmaf(f, x.x, v.x);
+        v.y = fmaf(f, x.y, v.y);
+        v.z = fmaf(f, x.z, v.z);
+        v.w = fmaf(f, x.w, v.w);
+      }
+      if (all) {
+        store_row<T, D>(a, w.t0 + (r >> a.b.g_shift), h * G + (r & (G - 1)), c4, v, M, L);
+      } else {
+        *reinterpret_cast<float4*>(part + r * D + 4 * c4) = v;
+        if (c4 == 0) *reinterpret_cast<float2*>(part + kRows * D + 2 * r) = make_float2(M, L);
+      }
+    }
+    __syncthreads();
+    if (!all) {
+      // the parts of the stream lie with CTAs first..last; the last to arrive merges them
+      const int first = share_of(stream, U, N), last = share_of(stream + w.units - 1, U, N);
+      const int parts = last - first + 1;
+      if (tid == 0) sh32[1] = count_acq_rel(a.counters + first) == (uint32_t)(parts - 1);
+      __syncthreads();
+      if (sh32[1]) {
+        if (tid == 0) a.counters[first] = 0;
+        // a CTA holds the stream in its first slot unless its share begins before it
+        const float* p0 = a.parts + (int64_t)(2 * first + (share_begin(first, U, N) < stream ? 1 : 0)) * part_floats(D);
+        const float* p1 = a.parts + (int64_t)(2 * (first + 1)) * part_floats(D);
+        auto at = [&](int k) { return k == 0 ? p0 : p1 + (int64_t)(2 * (k - 1)) * part_floats(D); };
+        float* wt = merge;  // weight of part k for row r at [r * kMaxParts + k]
+        for (int r = warp; r < R; r += NW) {
+          float M = -INFINITY, L = 0.f;
+          for (int k = lane; k < parts; k += 32) M = fmaxf(M, __ldcg(at(k) + kRows * D + 2 * r));
+#pragma unroll
+          for (int k = 16; k; k >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, k));
+          const float mu = M == -INFINITY ? 0.f : M;
+          for (int k = lane; k < parts; k += 32) {
+            const float2 x = __ldcg(reinterpret_cast<const float2*>(at(k) + kRows * D + 2 * r));
+            const float f = ex2(x.x - mu);
+            wt[r * kMaxParts + k] = f;
+            L = fmaf(f, x.y, L);
+          }
+#pragma unroll
+          for (int k = 16; k; k >>= 1) L += __shfl_xor_sync(0xffffffffu, L, k);
+          if (lane == 0) {
+            ml[0][r][0] = M;
+            ml[0][r][1] = L;
+          }
+        }
+        __syncthreads();
+        for (int it = tid; it < R * (D / 4); it += NW * 32) {
+          const int r = it / (D / 4), c4 = it % (D / 4);
+          float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
+          for (int k = 0; k < parts; ++k) {
+            const float4 x = __ldcg(reinterpret_cast<const float4*>(at(k) + r * D + 4 * c4));
+            const float f = wt[r * kMaxParts + k];
+            v.x = fmaf(f, x.x, v.x);
+            v.y = fmaf(f, x.y, v.y);
+            v.z = fmaf(f, x.z, v.z);
+            v.w = fmaf(f, x.w, v.w);
+          }
+          store_row<T, D>(a, w.t0 + (r >> a.b.g_shift), h * G + (r & (G - 1)), c4, v, ml[0][r][0], ml[0][r][1]);
+        }
+        __syncthreads();
+      }
+    }
+    // ---- on to the next stream of the share
+    u += i_end - i_begin;
+    if (u < u1) {
+      const int64_t seq_units = (int64_t)w.units * a.b.hkv;
+      const int b = cur.b;
+      cur.i = i_end - 1;
+      cur.next(a);
+      if (cur.b != b) base += seq_units;
+    }
+  }
+}
+
+template <class T, int D>
+cudaError_t launch(const CUtensorMap& km, const CUtensorMap& vm, const PagedAttnArgs& a, cudaStream_t s) {
+  static_assert(Cfg<D>::SMEM <= 227 * 1024 - 1024, "shared memory");
+  static_assert(Cfg<D>::MERGE >= kRows * kMaxParts * 4, "weights of the last merge fit the merge buffer");
+  static_assert(NW * Cfg<D>::S <= NW * 32, "one thread initialises each barrier");
+  const cudaError_t e =
+      cudaFuncSetAttribute(paged_decode_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<D>::SMEM);
+  if (e != cudaSuccess) return e;
+  paged_decode_kernel<T, D><<<a.n_ctas, NW * 32, Cfg<D>::SMEM, s>>>(km, vm, a);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_paged_decode(const CUtensorMap& km, const CUtensorMap& vm, const PagedAttnArgs& a, int head_dim,
+                                int dtype, cudaStream_t s) {
+  if (head_dim == 128) return dtype == 0 ? launch<Bf16, 128>(km, vm, a, s) : launch<Fp16, 128>(km, vm, a, s);
+  return dtype == 0 ? launch<Bf16, 64>(km, vm, a, s) : launch<Fp16, 64>(km, vm, a, s);
+}
+
+}  // namespace rq

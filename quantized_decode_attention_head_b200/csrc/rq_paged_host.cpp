@@ -3,6 +3,7 @@
 #include <cmath>
 #include <new>
 
+#include <cuda.h>
 #include <cuda_runtime.h>
 
 #include "rq.h"
@@ -12,6 +13,9 @@ struct rq_paged_cache {
   rq_paged_config cfg;
   int page_shift, g_shift;
   uint16_t *k, *v;
+  int sms;
+  bool mapped;
+  CUtensorMap k32, v32;  // boxes of the decode kernel: 64 channels of 32 tokens (or of a page, if shorter)
 };
 
 namespace {
@@ -54,7 +58,54 @@ rq_status fill_batch(const rq_paged_cache* c, int layer, const rq_paged_batch* b
 
 bool good_stride(int64_t stride, int heads, int d) { return stride >= (int64_t)heads * d && stride % 8 == 0; }
 
+// Workspace: status word, counters, the decode kernel's partial states.  The
+// offsets do not depend on the batch, so calls of different batches may share
+// a workspace one after another.
 constexpr size_t kStatusBytes = 256;
+constexpr size_t kCounterBytes = (rq::kMaxParts * 4 + 255) / 256 * 256;
+size_t parts_bytes(const rq_paged_cache* c) {
+  return (size_t)2 * rq::kMaxParts * rq::part_floats(c->cfg.head_dim) * 4;
+}
+
+int decode_ctas(const rq_paged_cache* c) { return c->sms < rq::kMaxParts ? c->sms : rq::kMaxParts; }
+
+typedef CUresult (*EncodeTiled)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                                const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                                CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+// The pages as a matrix [rows][head_dim], read in boxes of 64 channels (128
+// bytes, swizzled) and `rows` rows.
+bool encode(EncodeTiled fn, const rq_paged_cache* c, void* base, int box_rows, CUtensorMap* map) {
+  const rq_paged_config& f = c->cfg;
+  const cuuint64_t dims[2] = {(cuuint64_t)f.head_dim,
+                              (cuuint64_t)f.n_layers * f.n_pages * f.n_kv_heads * f.page_size};
+  const cuuint64_t strides[1] = {(cuuint64_t)f.head_dim * 2};
+  const cuuint32_t box[2] = {64, (cuuint32_t)box_rows};
+  const cuuint32_t elem[2] = {1, 1};
+  return fn(map, f.dtype == 0 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, base, dims,
+            strides, box, elem, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Tensor maps of the pages and the device's size, at the first attention call.
+rq_status prepare(rq_paged_cache* c) {
+  if (c->mapped) return RQ_OK;
+  void* fn = nullptr;
+  cudaDriverEntryPointQueryResult found;
+  const cudaError_t e = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault, &found);
+  if (e != cudaSuccess) return cuda_status(e);
+  if (!fn || found != cudaDriverEntryPointSuccess) return cuda_status(cudaErrorNotSupported);
+  int dev = 0;
+  cudaError_t d = cudaGetDevice(&dev);
+  if (d == cudaSuccess) d = cudaDeviceGetAttribute(&c->sms, cudaDevAttrMultiProcessorCount, dev);
+  if (d != cudaSuccess) return cuda_status(d);
+  const EncodeTiled enc = reinterpret_cast<EncodeTiled>(fn);
+  const int box = c->cfg.page_size < 32 ? c->cfg.page_size : 32;
+  if (!encode(enc, c, c->k, box, &c->k32) || !encode(enc, c, c->v, box, &c->v32))
+    return cuda_status(cudaErrorInvalidValue);
+  c->mapped = true;
+  return RQ_OK;
+}
 
 rq_status attention(rq_paged_cache* c, int layer, const rq_paged_batch* batch, const int* prefix, int prefix_len,
                     const void* q, int64_t q_stride, void* out, float* lse, float softmax_scale, int window,
@@ -72,6 +123,20 @@ rq_status attention(rq_paged_cache* c, int layer, const rq_paged_batch* batch, c
   if (rq_paged_workspace_bytes(c, batch->n_seqs, batch->n_tokens, &need) != RQ_OK) return RQ_ERR_INVALID_ARG;
   if (ws_bytes < need) return RQ_ERR_WORKSPACE;
   if (batch->n_tokens == 0 || batch->n_seqs == 0) return RQ_OK;
+  // positions are counted in 32 bits
+  const int64_t most = (int64_t)prefix_len + (int64_t)batch->table_width * c->cfg.page_size;
+  if (most + batch->n_tokens > 0x7FFFFFFF) return RQ_ERR_UNSUPPORTED;
+  if (window > most) window = 0;  // wider than any sequence
+  if (n_sink > most) n_sink = (int)most;
+  const rq_status pr = prepare(c);
+  if (pr != RQ_OK) return pr;
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  a.counters = reinterpret_cast<uint32_t*>(ws + kStatusBytes);
+  a.parts = reinterpret_cast<float*>(ws + kStatusBytes + kCounterBytes);
+  a.rows_o = a.rows_ml = nullptr;
+  a.row_slot = 0;
+  a.n_ctas = decode_ctas(c);
+  a.few_rows_only = (int64_t)batch->max_new << c->g_shift <= rq::kDecodeRows;
   a.b.status = static_cast<int*>(workspace);
   a.k_pages = c->k;
   a.v_pages = c->v;
@@ -85,6 +150,8 @@ rq_status attention(rq_paged_cache* c, int layer, const rq_paged_batch* batch, c
   a.n_sink = n_sink;
   a.prefix = prefix_len > 0 ? prefix : nullptr;
   a.prefix_len = prefix_len;
+  if (a.few_rows_only && prefix_len == 0)
+    return cuda_status(rq::launch_paged_decode(c->k32, c->v32, a, c->cfg.head_dim, c->cfg.dtype, stream));
   return cuda_status(rq::launch_paged_attention(a, c->cfg.head_dim, c->cfg.dtype, stream));
 }
 
@@ -168,7 +235,7 @@ rq_status rq_paged_append(rq_paged_cache* c, int layer, const rq_paged_batch* ba
 
 rq_status rq_paged_workspace_bytes(const rq_paged_cache* c, int n_seqs, int n_tokens, size_t* bytes) {
   if (!c || !bytes || n_seqs < 0 || n_tokens < 0) return RQ_ERR_INVALID_ARG;
-  *bytes = kStatusBytes;
+  *bytes = kStatusBytes + kCounterBytes + parts_bytes(c);
   return RQ_OK;
 }
 
