@@ -19,7 +19,7 @@ LIB = os.path.join(PKG, "librq.so")
 # the decode kernel is instantiated once per (head_dim, GQA group) pair in its
 # own translation unit, so the units compile in parallel
 SOURCES = ["rq_alloc.cpp", "rq_host.cpp", "rq_quantize.cu", "rq_decode.cu", "rq_paged_host.cpp",
-           "rq_paged_append.cu", "rq_paged_attn.cu", "rq_paged_decode.cu"] + [
+           "rq_paged_append.cu", "rq_paged_decode.cu", "rq_paged_prompt.cu"] + [
     f"rq_decode_{d}x{g}.cu" for d in (128, 64) for g in (1, 2, 4, 8)]
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 

@@ -15,6 +15,7 @@ __device__ __forceinline__ void flag_index(int* status) {
 
 // 16-bit element types of the pages: conversions to and from fp32.
 struct Bf16 {
+  static constexpr int kType = 1;  // of tcgen05 instruction descriptors
   static __device__ __forceinline__ float2 unpack(uint32_t u) {
     return make_float2(__uint_as_float(u << 16), __uint_as_float(u & 0xFFFF0000u));
   }
@@ -24,6 +25,7 @@ struct Bf16 {
   }
 };
 struct Fp16 {
+  static constexpr int kType = 0;
   static __device__ __forceinline__ float2 unpack(uint32_t u) {
     return __half22float2(*reinterpret_cast<const __half2*>(&u));
   }

@@ -55,6 +55,8 @@ struct PagedAttnArgs {
   int n_sink;
   const int* prefix;      // pages of the shared prefix, or null
   int prefix_len;
+  int over_prefix;        // prompt kernel: all rows of the batch over the prefix
+  int few_rows_apart;     // sequences of at most kDecodeRows rows are the decode kernel's
   int few_rows_only;      // the call said that no sequence has more than 16 rows a kv head
   int n_ctas;             // CTAs of the decode kernel, at most kMaxParts
   float* parts;           // its partial states: two slots of part_floats(D) a CTA
@@ -66,6 +68,8 @@ struct PagedAttnArgs {
 
 // Most CTAs among which one stream of the decode kernel can be split.
 constexpr int kMaxParts = 160;
+constexpr int kPromptRows = 256;  // rows of a CTA of the prompt kernel
+constexpr int kMaxSplits = 128;   // CTAs among which it splits the keys of the same rows
 constexpr int kDecodeRows = 16;  // rows of a kv head that the decode kernel takes
 // o[16][D], then (m, l) of each row
 __host__ __device__ constexpr int part_floats(int D) { return kDecodeRows * D + 2 * kDecodeRows; }
@@ -73,6 +77,9 @@ __host__ __device__ constexpr int part_floats(int D) { return kDecodeRows * D + 
 cudaError_t launch_paged_append(const PagedAppendArgs& a, int head_dim, int dtype, cudaStream_t s);
 cudaError_t launch_paged_decode(const CUtensorMap& km, const CUtensorMap& vm, const PagedAttnArgs& a, int head_dim,
                                 int dtype, cudaStream_t s);
-cudaError_t launch_paged_attention(const PagedAttnArgs& a, int head_dim, int dtype, cudaStream_t s);
+cudaError_t launch_paged_prompt(const CUtensorMap& km, const CUtensorMap& vm, const PagedAttnArgs& a, int blocks,
+                                int splits, int head_dim, int dtype, cudaStream_t s);
+// Merges slots [0, shared) and the rows' own (one of the decode kernel or `own` of the prompt kernel).
+cudaError_t launch_paged_merge(const PagedAttnArgs& a, int shared, int own, int head_dim, int dtype, cudaStream_t s);
 
 }  // namespace rq

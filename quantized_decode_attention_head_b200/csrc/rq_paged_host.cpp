@@ -16,6 +16,7 @@ struct rq_paged_cache {
   int sms;
   bool mapped;
   CUtensorMap k32, v32;  // boxes of the decode kernel: 64 channels of 32 tokens (or of a page, if shorter)
+  CUtensorMap kp, vp;    // boxes of the prompt kernel: 64 channels of a page
 };
 
 namespace {
@@ -67,6 +68,15 @@ size_t parts_bytes(const rq_paged_cache* c) {
   return (size_t)2 * rq::kMaxParts * rq::part_floats(c->cfg.head_dim) * 4;
 }
 
+// Rows of partial states that one pass of the prompt kernel may write: its
+// splits keep CTAs (256 rows a kv head each) at or below one a SM.
+int64_t part_rows(const rq_paged_cache* c, int n_tokens) {
+  const int64_t rows = (int64_t)n_tokens * c->cfg.n_q_heads;
+  const int64_t most = (int64_t)rq::kMaxParts * rq::kPromptRows;
+  const int64_t split = rows * rq::kMaxSplits < most ? rows * rq::kMaxSplits : most;
+  return rows > split ? rows : split;
+}
+
 int decode_ctas(const rq_paged_cache* c) { return c->sms < rq::kMaxParts ? c->sms : rq::kMaxParts; }
 
 typedef CUresult (*EncodeTiled)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
@@ -101,10 +111,27 @@ rq_status prepare(rq_paged_cache* c) {
   if (d != cudaSuccess) return cuda_status(d);
   const EncodeTiled enc = reinterpret_cast<EncodeTiled>(fn);
   const int box = c->cfg.page_size < 32 ? c->cfg.page_size : 32;
-  if (!encode(enc, c, c->k, box, &c->k32) || !encode(enc, c, c->v, box, &c->v32))
+  const int page = c->cfg.page_size;
+  if (!encode(enc, c, c->k, box, &c->k32) || !encode(enc, c, c->v, box, &c->v32) ||
+      !encode(enc, c, c->k, page, &c->kp) || !encode(enc, c, c->v, page, &c->vp))
     return cuda_status(cudaErrorInvalidValue);
   c->mapped = true;
   return RQ_OK;
+}
+
+// CTAs among which the prompt kernel divides the keys of the same rows: as
+// many as fill the device once, while each keeps at least four tiles of 128 keys.
+int splits_of(const rq_paged_cache* c, int64_t blocks, int64_t keys, int window, int n_sink, int max_new) {
+  const int64_t ctas = blocks * c->cfg.n_kv_heads;
+  const int64_t sms = decode_ctas(c);
+  if (ctas <= 0) return 1;
+  const int64_t reach = (int64_t)window + n_sink + max_new;
+  if (window > 0 && reach < keys) keys = reach;
+  int64_t s = sms / ctas;
+  const int64_t by_work = (keys + 511) / 512;
+  if (s > by_work) s = by_work;
+  if (s > rq::kMaxSplits) s = rq::kMaxSplits;
+  return s < 1 ? 1 : (int)s;
 }
 
 rq_status attention(rq_paged_cache* c, int layer, const rq_paged_batch* batch, const int* prefix, int prefix_len,
@@ -134,7 +161,7 @@ rq_status attention(rq_paged_cache* c, int layer, const rq_paged_batch* batch, c
   a.counters = reinterpret_cast<uint32_t*>(ws + kStatusBytes);
   a.parts = reinterpret_cast<float*>(ws + kStatusBytes + kCounterBytes);
   a.rows_o = a.rows_ml = nullptr;
-  a.row_slot = 0;
+  a.row_slot = a.over_prefix = 0;
   a.n_ctas = decode_ctas(c);
   a.few_rows_only = (int64_t)batch->max_new << c->g_shift <= rq::kDecodeRows;
   a.b.status = static_cast<int*>(workspace);
@@ -150,9 +177,47 @@ rq_status attention(rq_paged_cache* c, int layer, const rq_paged_batch* batch, c
   a.n_sink = n_sink;
   a.prefix = prefix_len > 0 ? prefix : nullptr;
   a.prefix_len = prefix_len;
-  if (a.few_rows_only && prefix_len == 0)
-    return cuda_status(rq::launch_paged_decode(c->k32, c->v32, a, c->cfg.head_dim, c->cfg.dtype, stream));
-  return cuda_status(rq::launch_paged_attention(a, c->cfg.head_dim, c->cfg.dtype, stream));
+  const int d = c->cfg.head_dim, type = c->cfg.dtype;
+  const int64_t all_rows = (int64_t)batch->n_tokens << c->g_shift;  // of one kv head
+
+  // Which kernels: sequences of at most 16 rows a kv head go to the decode
+  // kernel, which splits the tokens evenly whatever the lengths, the others
+  // to the prompt kernel; when no sequence can have few rows (one sequence,
+  // or all as long as they may be) the decode kernel is not launched.
+  const bool decode = a.few_rows_only || (batch->n_seqs > 1 && (int64_t)batch->n_seqs * batch->max_new != batch->n_tokens);
+  const bool prompt = !a.few_rows_only;
+  a.few_rows_apart = decode;
+  int own = 0, shared = 0;
+  int64_t blocks = 0;
+  if (prompt) {
+    const int64_t seqs = decode ? all_rows / (rq::kDecodeRows + 1) : all_rows;  // that can have a block of their own
+    blocks = all_rows / rq::kPromptRows + (seqs < batch->n_seqs ? seqs : batch->n_seqs);
+    own = splits_of(c, blocks, (int64_t)batch->table_width * c->cfg.page_size, window, n_sink, batch->max_new);
+  }
+  const int64_t shared_blocks = (all_rows + rq::kPromptRows - 1) / rq::kPromptRows;
+  if (prefix_len > 0) shared = splits_of(c, shared_blocks, prefix_len, 0, 0, 0);
+  if (blocks > 0x7FFFFFFF || shared_blocks > 0x7FFFFFFF) return RQ_ERR_UNSUPPORTED;
+  const bool merge = shared > 0 || own > 1;
+  if (merge) {
+    a.rows_o = reinterpret_cast<float*>(ws + kStatusBytes + kCounterBytes + parts_bytes(c));
+    a.rows_ml = a.rows_o + 2 * part_rows(c, batch->n_tokens) * d;
+  }
+  cudaError_t e = cudaSuccess;
+  if (shared > 0) {
+    a.over_prefix = 1;
+    e = rq::launch_paged_prompt(c->kp, c->vp, a, (int)shared_blocks, shared, d, type, stream);
+    a.over_prefix = 0;
+    a.row_slot = shared;
+  }
+  if (e == cudaSuccess && prompt && blocks > 0)
+    e = rq::launch_paged_prompt(c->kp, c->vp, a, (int)blocks, own, d, type, stream);
+  if (e == cudaSuccess && decode) {
+    rq::PagedAttnArgs f = a;
+    if (shared == 0) f.rows_o = f.rows_ml = nullptr;  // straight to out
+    e = rq::launch_paged_decode(c->k32, c->v32, f, d, type, stream);
+  }
+  if (e == cudaSuccess && merge) e = rq::launch_paged_merge(a, shared, own, d, type, stream);
+  return cuda_status(e);
 }
 
 }  // namespace
@@ -171,7 +236,7 @@ rq_status rq_paged_cache_init(const rq_paged_config* cfg, void* k_pages, void* v
   const int g = cfg->n_q_heads / cfg->n_kv_heads;
   if (g != 1 && g != 2 && g != 4 && g != 8) return RQ_ERR_UNSUPPORTED;
   const double rows = (double)cfg->n_layers * cfg->n_pages * cfg->n_kv_heads * cfg->page_size;
-  if (rows >= 2147483648.0 || cfg->n_kv_heads > 65535) return RQ_ERR_UNSUPPORTED;
+  if (rows >= 2147483648.0 || cfg->n_kv_heads > 8192) return RQ_ERR_UNSUPPORTED;
   rq_paged_cache* c = new (std::nothrow) rq_paged_cache();
   if (!c) return RQ_ERR_INVALID_ARG;
   c->cfg = *cfg;
@@ -235,7 +300,9 @@ rq_status rq_paged_append(rq_paged_cache* c, int layer, const rq_paged_batch* ba
 
 rq_status rq_paged_workspace_bytes(const rq_paged_cache* c, int n_seqs, int n_tokens, size_t* bytes) {
   if (!c || !bytes || n_seqs < 0 || n_tokens < 0) return RQ_ERR_INVALID_ARG;
-  *bytes = kStatusBytes + kCounterBytes + parts_bytes(c);
+  // the shared prefix and what follows it are one pass each
+  *bytes = kStatusBytes + kCounterBytes + parts_bytes(c) +
+           (size_t)(2 * part_rows(c, n_tokens)) * (c->cfg.head_dim + 2) * 4;
   return RQ_OK;
 }
 

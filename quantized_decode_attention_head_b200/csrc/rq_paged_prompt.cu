@@ -1,0 +1,671 @@
+// Attention of many query rows over the paged 16-bit cache (sm_100a): prompts
+// and pieces of prompts, and all queries of a batch over the prefix they share.
+//
+// A CTA takes 256 query rows of one kv head (two tiles of 128; a row is a
+// token and one of the G heads, so the heads of a group share every key they
+// read) and walks over tiles of 128 keys.  Both products run on tcgen05 with
+// the accumulators in TMEM:
+//   S_t = Q_t K^T     (A and B from shared memory, K-major)
+//   O_t += P_t V      (A = P_t from TMEM, B = V from shared memory, MN-major)
+// One warp issues TMA copies of the pages (64-channel boxes, 128-byte swizzle),
+// one warp issues the MMAs, and a group of four warps per tile does the
+// softmax, one thread a row: no shuffles.  The MMA warp alternates between the
+// tiles, so one tile's products run while the other's weights are computed.
+// P_t overwrites S_t (16-bit pairs, half its columns).  TMEM columns:
+// [S_0 | S_1 | O_0 | O_1].  The running maximum moves only when a row's scores
+// exceed it by 2^8 (a weight then stays below 256, exact in the type's
+// exponent), so O is rarely rescaled; sums are fp32 of the unrounded weights.
+//
+// Bound: 4 * 128 * 128 * D flops a tile pair on the tensor cores against
+// 128 * 128 exponentials (16 a clock an SM): about equal at D = 128.
+#include <cuda.h>
+
+#include <climits>
+
+#include "rq_paged.cuh"
+
+namespace rq {
+namespace {
+
+constexpr int kTileRows = 128;
+constexpr int kBlockRows = kPromptRows;
+constexpr int kKeys = 128;  // keys a step
+constexpr int kThreads = 384;
+static_assert(kBlockRows == 2 * kTileRows, "two tiles a CTA");
+
+template <int D>
+struct Cfg {
+  static constexpr int P = D / 64;                  // 64-channel panels
+  static constexpr int PANEL = 128 * 128;           // bytes: 128 rows of 64 channels
+  static constexpr int TILE = P * PANEL;
+  static constexpr int NS = D == 128 ? 2 : 4;       // stages of keys, and of values
+  static constexpr int SMEM = 1024 + 2 * TILE + 2 * NS * TILE;
+  static constexpr int COLS = 512;                  // TMEM columns: 2 x 128 (S) + 2 x D (O), up to a power of two
+};
+
+// ------------------------------------------------------------------ tcgen05
+__device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;\n" ::: "memory"); }
+__device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;\n" ::: "memory"); }
+__device__ __forceinline__ void tc_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;\n" ::: "memory"); }
+
+// Arrives on bar when every tcgen05 operation this thread issued before is complete.
+__device__ __forceinline__ void tc_commit(uint64_t* bar) {
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n" ::"r"(smem_u32(bar))
+               : "memory");
+}
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool acc) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"((int)acc)
+      : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool acc) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"((int)acc)
+      : "memory");
+}
+
+#define RQ_OUT(i) "=r"(r[i])
+#define RQ_IN(i) "r"(r[i])
+#define RQ_TIE(i) "+r"(r[i])
+#define RQ_32(M)                                                                                                    \
+  M(0), M(1), M(2), M(3), M(4), M(5), M(6), M(7), M(8), M(9), M(10), M(11), M(12), M(13), M(14), M(15), M(16),      \
+      M(17), M(18), M(19), M(20), M(21), M(22), M(23), M(24), M(25), M(26), M(27), M(28), M(29), M(30), M(31)
+
+// 32 columns of this thread's TMEM lane (the warp's 32 lanes at addr).
+__device__ __forceinline__ void tc_ld32(uint32_t (&r)[32], uint32_t addr) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,"
+      "%29,%30,%31}, [%32];\n"
+      : RQ_32(RQ_OUT)
+      : "r"(addr));
+}
+__device__ __forceinline__ void tc_st32(uint32_t addr, const uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,"
+      "%29,%30,%31};\n" ::RQ_32(RQ_IN),
+      "r"(addr)
+      : "memory");
+}
+
+// Waits for this thread's TMEM loads.  The loaded registers pass through, so
+// that no use of them can be moved before the wait.
+__device__ __forceinline__ void tc_wait_ld(uint32_t (&r)[32]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;\n" : RQ_32(RQ_TIE)::"memory");
+}
+
+// Shared-memory matrix descriptor: 128-byte swizzle, strides in bytes.
+__device__ __forceinline__ uint64_t smem_desc(uint32_t addr, uint32_t lbo, uint32_t sbo) {
+  return (uint64_t)((addr & 0x3FFFF) >> 4) | (uint64_t)(lbo >> 4) << 16 | (uint64_t)(sbo >> 4) << 32 |
+         (uint64_t)1 << 46 | (uint64_t)2 << 61;
+}
+// Instruction descriptor: fp32 accumulator, A and B of the pages' type (0
+// fp16, 1 bf16), B K-major or MN-major.
+__host__ __device__ constexpr uint32_t instr_desc(int type, bool b_mn, int m, int n) {
+  return 1u << 4 | (uint32_t)type << 7 | (uint32_t)type << 10 | (uint32_t)b_mn << 16 | (uint32_t)(n >> 3) << 17 |
+         (uint32_t)(m >> 4) << 24;
+}
+
+__device__ __forceinline__ void tma_box(uint32_t dst, const CUtensorMap* map, int x, int y, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];\n" ::"r"(
+          dst),
+      "l"(map), "r"(x), "r"(y), "r"(smem_u32(bar))
+      : "memory");
+}
+
+// A warp's wait: all lanes go on, or none (the tcgen05 accesses need the whole warp).
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity) {
+  return __all_sync(0xffffffffu, mbar_wait_bounded(bar, parity));
+}
+
+struct Shared {
+  uint64_t k_full[4], k_empty[4], v_full[4], v_empty[4];
+  uint64_t s_full[2], p_ready[2], o_final[2];
+  uint32_t tmem;
+  int seq, block;          // the CTA's sequence and row block in it
+  int row_token[kBlockRows];  // packed token, -1: no row
+  int row_p[kBlockRows];      // position of the row's query
+  int p_min[8], p_max[8];     // of each warp's 32 rows
+  int dead;
+};
+
+// The keys a CTA walks over, as tokens of its page list: tiles [0, ns) and
+// [lo_t, lo_t + tiles - ns), of which this split takes [t0, t1).
+struct Keys {
+  int base;  // position of key 0
+  int end;   // keys there are
+  int lo, hi, sink;  // keys [lo, hi) and [0, sink) are seen by some row
+  int ns, lo_t, t0, t1;
+  const int* pages;
+};
+__device__ __forceinline__ int key_of(const Keys& k, int tile) {
+  return kKeys * (tile < k.ns ? tile : k.lo_t + tile - k.ns);
+}
+
+template <class T, int D>
+__global__ void __launch_bounds__(kThreads, 1)
+    paged_prompt_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
+                        const __grid_constant__ PagedAttnArgs a) {
+  using C = Cfg<D>;
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ Shared sh;
+  uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const uint32_t q_sm = smem_u32(sm), k_sm = q_sm + 2 * C::TILE, v_sm = k_sm + C::NS * C::TILE;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int h = blockIdx.y, G = 1 << a.b.g_shift;
+
+  // ---- which rows
+  int row0 = 0, rows = 0;
+  Seq seq = {0, 0, 0};
+  if (a.over_prefix) {
+    row0 = blockIdx.x * kBlockRows;
+    rows = a.b.n_tokens << a.b.g_shift;
+  } else {
+    // the last blocks first: they see the most keys
+    const int want = gridDim.x - 1 - blockIdx.x;
+    if (warp == 0) {
+      int before = 0, found = -1, block = 0;
+      for (int b0 = 0; b0 < a.b.n_seqs && found < 0; b0 += 32) {
+        int x = 0;
+        if (b0 + lane < a.b.n_seqs) {
+          const Seq s = load_seq(a.b, b0 + lane);
+          const int r = s.n << a.b.g_shift;
+          if (!(a.few_rows_apart && r <= kDecodeRows)) x = (r + kBlockRows - 1) / kBlockRows;
+        }
+        const int v = x;
+#pragma unroll
+        for (int k = 1; k < 32; k <<= 1) {
+          const int y = __shfl_up_sync(0xffffffffu, x, k);
+          if (lane >= k) x += y;
+        }
+        const uint32_t hit = __ballot_sync(0xffffffffu, want >= before + x - v && want < before + x);
+        if (hit) {
+          const int src = __ffs(hit) - 1;
+          found = b0 + src;
+          block = want - before - __shfl_sync(0xffffffffu, x - v, src);
+        }
+        before += __shfl_sync(0xffffffffu, x, 31);
+      }
+      if (lane == 0) {
+        sh.seq = found;
+        sh.block = block;
+      }
+    }
+    __syncthreads();
+    if (sh.seq < 0) return;
+    seq = load_seq(a.b, sh.seq);
+    row0 = sh.block * kBlockRows;
+    rows = seq.n << a.b.g_shift;
+  }
+  if (tid == 0) {
+    for (int i = 0; i < C::NS; ++i) {
+      mbar_init(&sh.k_full[i], 1);
+      mbar_init(&sh.k_empty[i], 1);
+      mbar_init(&sh.v_full[i], 1);
+      mbar_init(&sh.v_empty[i], 1);
+    }
+    for (int t = 0; t < 2; ++t) {
+      mbar_init(&sh.s_full[t], 1);
+      mbar_init(&sh.p_ready[t], kTileRows);
+      mbar_init(&sh.o_final[t], 1);
+    }
+    mbar_fence_init();
+    sh.dead = 0;
+  }
+  if (warp == 1) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;\n" ::"r"(smem_u32(&sh.tmem)),
+                 "r"(C::COLS)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;\n");
+  }
+  if (tid < kBlockRows) {
+    const int r = row0 + tid;
+    int token = -1, p = 0;
+    if (r < rows) {
+      token = r >> a.b.g_shift;
+      if (a.over_prefix) {
+        const int b = seq_of(a.b, token);
+        if (b >= 0) {
+          const Seq s = load_seq(a.b, b);
+          if (token >= s.t0 && token < s.t0 + s.n)
+            p = a.prefix_len + s.len - s.n + (token - s.t0);
+          else
+            token = -1;
+        } else {
+          token = -1;
+        }
+      } else {
+        p = a.prefix_len + seq.len - seq.n + token;
+        token += seq.t0;
+      }
+    }
+    sh.row_token[tid] = token;
+    sh.row_p[tid] = p;
+    int lo = token >= 0 ? p : INT_MAX - 1, hi = token >= 0 ? p : INT_MIN;
+#pragma unroll
+    for (int k = 16; k; k >>= 1) {
+      lo = min(lo, __shfl_xor_sync(0xffffffffu, lo, k));
+      hi = max(hi, __shfl_xor_sync(0xffffffffu, hi, k));
+    }
+    if (lane == 0) {
+      sh.p_min[warp] = lo;
+      sh.p_max[warp] = hi;
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = sh.tmem;
+  int p_lo[2], p_hi[2];
+#pragma unroll
+  for (int t = 0; t < 2; ++t) {
+    p_lo[t] = min(min(sh.p_min[4 * t], sh.p_min[4 * t + 1]), min(sh.p_min[4 * t + 2], sh.p_min[4 * t + 3]));
+    p_hi[t] = max(max(sh.p_max[4 * t], sh.p_max[4 * t + 1]), max(sh.p_max[4 * t + 2], sh.p_max[4 * t + 3]));
+  }
+  const int tiles_q = p_hi[1] != INT_MIN ? 2 : (p_hi[0] != INT_MIN ? 1 : 0);  // row tiles with any row
+
+  // ---- which keys
+  Keys key;
+  key.base = a.over_prefix ? 0 : a.prefix_len;
+  key.end = a.over_prefix ? a.prefix_len : seq.len;
+  key.pages = a.over_prefix ? a.prefix : a.b.table + (int64_t)sh.seq * a.b.width;
+  {
+    const int first = min(p_lo[0], p_lo[1]), last = max(p_hi[0], p_hi[1]);
+    int hi = tiles_q ? last + 1 - key.base : 0;
+    hi = hi < 0 ? 0 : (hi > key.end ? key.end : hi);
+    int lo = a.window > 0 && tiles_q ? first + 1 - a.window - key.base : 0;
+    lo = lo < 0 ? 0 : (lo > hi ? hi : lo);
+    int sink = a.window > 0 ? a.n_sink - key.base : 0;
+    key.sink = sink < 0 ? 0 : (sink > hi ? hi : sink);
+    key.lo = lo;
+    key.hi = hi;
+    key.lo_t = lo / kKeys;
+    const int st = (key.sink + kKeys - 1) / kKeys;
+    key.ns = st < key.lo_t ? st : key.lo_t;
+    const int n = key.ns + (hi + kKeys - 1) / kKeys - key.lo_t;
+    key.t0 = (int)((int64_t)n * blockIdx.z / gridDim.z);
+    key.t1 = (int)((int64_t)n * (blockIdx.z + 1) / gridDim.z);
+  }
+  const int n_steps = key.t1 - key.t0;
+
+  // ---- page numbers out of range anywhere in the walk: the masked path
+  bool bad = false;
+  {
+    const int per = kKeys >> a.b.page_shift;  // pages a tile
+    for (int i = tid; i < n_steps * per; i += kThreads) {
+      const int j = key_of(key, key.t0 + i / per) + ((i % per) << a.b.page_shift);
+      if (j < key.end && page_row(a.b, __ldg(key.pages + (j >> a.b.page_shift))) < 0) bad = true;
+    }
+  }
+
+  // ---- queries to shared memory, in the layout a TMA copy would give them
+  for (int i = tid; i < tiles_q * kTileRows * (D / 8); i += kThreads) {
+    const int r = i / (D / 8), c = i % (D / 8);
+    const int token = sh.row_token[r];
+    uint4 x = make_uint4(0, 0, 0, 0);
+    if (token >= 0)
+      x = __ldg(reinterpret_cast<const uint4*>(a.q + token * a.q_stride + (h * G + ((row0 + r) & (G - 1))) * D) + c);
+    const int rr = r & (kTileRows - 1);
+    *reinterpret_cast<uint4*>(sm + (r / kTileRows) * C::TILE + (c >> 3) * C::PANEL + rr * 128 +
+                              (((c & 7) ^ (rr & 7)) << 4)) = x;
+  }
+  fence_proxy_async_smem();
+  const bool any_bad = __syncthreads_or(bad);
+
+  if (n_steps > 0) {
+    if (warp == 0) {
+      // ------------------------------------------------ producer
+      if (lane == 0) {
+        const int per = kKeys >> a.b.page_shift, ps = 1 << a.b.page_shift;
+        const int head_row = h << a.b.page_shift;
+        bool ok = true;
+        for (int k = 0; k < n_steps && ok; ++k) {
+          const int slot = k % C::NS;
+          const uint32_t par = ((k / C::NS) & 1) ^ 1;
+          const int j = key_of(key, key.t0 + k);
+          int row[8];
+          uint32_t bytes = 0;
+#pragma unroll
+          for (int g = 0; g < 8; ++g) {
+            row[g] = -1;
+            const int jj = j + (g << a.b.page_shift);
+            if (g < per && jj < key.end) {
+              const int64_t r = page_row(a.b, __ldg(key.pages + (jj >> a.b.page_shift)));
+              if (r >= 0) {
+                row[g] = (int)r + head_row;
+                bytes += ps * D * 2;
+              }
+            }
+          }
+#pragma unroll
+          for (int kv = 0; kv < 2 && ok; ++kv) {
+            uint64_t* full = kv ? &sh.v_full[slot] : &sh.k_full[slot];
+            ok = mbar_wait_bounded(kv ? &sh.v_empty[slot] : &sh.k_empty[slot], par);
+            if (!ok) break;
+            if (bytes)
+              mbar_arrive_expect_tx(full, bytes);
+            else
+              mbar_arrive(full);
+            const uint32_t dst = (kv ? v_sm : k_sm) + slot * C::TILE;
+#pragma unroll
+            for (int g = 0; g < 8; ++g)
+              if (row[g] >= 0) {
+#pragma unroll
+                for (int p = 0; p < C::P; ++p)
+                  tma_box(dst + p * C::PANEL + (g << a.b.page_shift) * 128, kv ? &vmap : &kmap, 64 * p, row[g], full);
+              }
+          }
+        }
+        if (!ok) sh.dead = 1;
+      }
+    } else if (warp == 1) {
+      // ------------------------------------------------ MMA issue
+      constexpr uint32_t id_s = instr_desc(T::kType, false, kTileRows, kKeys);
+      constexpr uint32_t id_o = instr_desc(T::kType, true, kTileRows, D);
+      auto scores = [&](int t, int slot) {
+        if (lane == 0) {
+#pragma unroll
+          for (int ks = 0; ks < D / 16; ++ks) {
+            const uint32_t off = (ks >> 2) * C::PANEL + (ks & 3) * 32;
+            mma_ss(tmem + t * kKeys, smem_desc(q_sm + t * C::TILE + off, 16, 1024),
+                   smem_desc(k_sm + slot * C::TILE + off, 16, 1024), id_s, ks > 0);
+          }
+          tc_commit(&sh.s_full[t]);
+        }
+      };
+      bool ok = warp_wait(&sh.k_full[0], 0);
+      if (ok) {
+        tc_fence_after();
+        for (int t = 0; t < tiles_q; ++t) scores(t, 0);
+        if (lane == 0) tc_commit(&sh.k_empty[0]);
+      }
+      for (int k = 0; k < n_steps && ok; ++k) {
+        const int slot = k % C::NS, next = (k + 1) % C::NS;
+        for (int t = 0; t < tiles_q && ok; ++t) {
+          if (t == 0) {
+            ok = warp_wait(&sh.v_full[slot], (k / C::NS) & 1);
+            // values that no row sees become zero: 0 * NaN would reach the sums
+            const int j = key_of(key, key.t0 + k);
+            if (ok && (any_bad || j + kKeys > key.hi || (j < key.lo && j + kKeys > key.sink))) {
+              for (int i = lane; i < kKeys; i += 32) {
+                const int jj = j + i;
+                bool live = jj < key.hi && (jj >= key.lo || jj < key.sink);
+                if (live && any_bad) live = page_row(a.b, __ldg(key.pages + (jj >> a.b.page_shift))) >= 0;
+                if (!live)
+#pragma unroll
+                  for (int c = 0; c < C::P * 8; ++c)
+                    *reinterpret_cast<uint4*>(sm + (v_sm - q_sm) + slot * C::TILE + (c >> 3) * C::PANEL + i * 128 +
+                                              (c & 7) * 16) = make_uint4(0, 0, 0, 0);
+              }
+              fence_proxy_async_smem();
+              __syncwarp();
+            }
+          }
+          ok = ok && warp_wait(&sh.p_ready[t], k & 1);
+          if (!ok) break;
+          tc_fence_after();
+          if (lane == 0) {
+#pragma unroll
+            for (int kt = 0; kt < kKeys / 16; ++kt)
+              mma_ts(tmem + 2 * kKeys + t * D, tmem + t * kKeys + kt * 8,
+                     smem_desc(v_sm + slot * C::TILE + kt * 2048, C::PANEL, 1024), id_o, k > 0 || kt > 0);
+            if (t == tiles_q - 1) tc_commit(&sh.v_empty[slot]);
+          }
+          if (k + 1 < n_steps) {
+            if (t == 0) {
+              ok = warp_wait(&sh.k_full[next], ((k + 1) / C::NS) & 1);
+              if (!ok) break;
+              tc_fence_after();
+            }
+            scores(t, next);
+            if (t == tiles_q - 1 && lane == 0) tc_commit(&sh.k_empty[next]);
+          } else if (lane == 0) {
+            tc_commit(&sh.o_final[t]);
+          }
+        }
+      }
+      if (!ok && lane == 0) sh.dead = 1;
+    }
+  }
+  if (warp >= 4 && (warp - 4) / 4 < tiles_q) {
+    // -------------------------------------------------- softmax, one row a thread
+    const int t = (warp - 4) / 4;
+    const int r = t * kTileRows + (warp & 3) * 32 + lane;
+    const int token = sh.row_token[r], p = sh.row_p[r];
+    const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+    const uint32_t s_at = tmem + t * kKeys + lanes, o_at = tmem + 2 * kKeys + t * D + lanes;
+    // keys the row sees: [w_lo, limit) and [0, sink), the latter below limit too
+    const int limit = token >= 0 ? min(key.end, p + 1 - key.base) : 0;
+    const int w_lo = a.window > 0 ? p + 1 - a.window - key.base : INT_MIN;
+    float m = -INFINITY, l = 0.f;
+    bool ok = true;
+    for (int k = 0; k < n_steps; ++k) {
+      const int j = key_of(key, key.t0 + k);
+      ok = warp_wait(&sh.s_full[t], k & 1);
+      if (!ok) break;
+      tc_fence_after();
+      uint32_t s[4][32];
+#pragma unroll
+      for (int c = 0; c < 4; ++c) tc_ld32(s[c], s_at + 32 * c);
+#pragma unroll
+      for (int c = 0; c < 4; ++c) tc_wait_ld(s[c]);
+      const bool whole = !any_bad && j + kKeys <= min(key.end, p_lo[t] + 1 - key.base) &&
+                         (a.window == 0 || j > p_hi[t] - a.window - key.base || j + kKeys <= key.sink);
+      if (!whole) {
+        uint32_t pages = 0xFFu;  // bit g: the page of keys 16 g.. of the tile exists
+        if (any_bad) {
+          pages = 0;
+          for (int g = 0; g < 8; ++g) {
+            const int jj = j + 16 * g;
+            if (jj < key.end && page_row(a.b, __ldg(key.pages + (jj >> a.b.page_shift))) >= 0) pages |= 1u << g;
+          }
+        }
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+#pragma unroll
+          for (int e = 0; e < 32; ++e) {
+            const int jj = j + 32 * c + e;
+            const bool see = jj < limit && (jj >= w_lo || jj < key.sink) && ((pages >> (2 * c + e / 16)) & 1u);
+            if (!see) s[c][e] = 0xFF800000u;
+          }
+      }
+      float mx = -INFINITY;
+#pragma unroll
+      for (int c = 0; c < 4; ++c)
+#pragma unroll
+        for (int e = 0; e < 32; ++e) mx = fmaxf(mx, __uint_as_float(s[c][e]));
+      mx *= a.scale_log2;
+      const bool move = mx > m + 8.0f;  // true at the first score of a row (m = -inf)
+      if (__any_sync(0xffffffffu, move)) {
+        const float mn = move ? mx : m;
+        const float alpha = move ? ex2(m - mn) : 1.f;
+        m = mn;
+        l *= alpha;
+        if (k > 0) {
+          // the product before this step's scores is complete (s_full follows it)
+#pragma unroll
+          for (int c = 0; c < D / 32; ++c) {
+            uint32_t o[32];
+            tc_ld32(o, o_at + 32 * c);
+            tc_wait_ld(o);
+#pragma unroll
+            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+            tc_st32(o_at + 32 * c, o);
+          }
+        }
+      }
+      const float mu = m == -INFINITY ? 0.f : m;
+      float sum0 = 0.f, sum1 = 0.f;
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        uint32_t w[32];
+#pragma unroll
+        for (int e = 0; e < 32; ++e) {
+          const uint32_t x = s[2 * c + e / 16][2 * (e % 16)], y = s[2 * c + e / 16][2 * (e % 16) + 1];
+          const float px = ex2(fmaf(__uint_as_float(x), a.scale_log2, -mu));
+          const float py = ex2(fmaf(__uint_as_float(y), a.scale_log2, -mu));
+          sum0 += px;
+          sum1 += py;
+          w[e] = T::pack(px, py);
+        }
+        tc_st32(s_at + 32 * c, w);
+      }
+      l += sum0 + sum1;
+      tc_wait_st();
+      tc_fence_before();
+      mbar_arrive(&sh.p_ready[t]);
+    }
+    if (ok && n_steps > 0) {
+      ok = warp_wait(&sh.o_final[t], 0);
+      tc_fence_after();
+    }
+    if (!ok) sh.dead = 1;
+    const int64_t row = (int64_t)token * a.b.hq + h * G + ((row0 + r) & (G - 1));
+    const int64_t at = (int64_t)(a.row_slot + blockIdx.z) * a.b.n_tokens * a.b.hq + row;
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+#pragma unroll
+    for (int c = 0; c < D / 32; ++c) {
+      uint32_t o[32];
+      if (n_steps > 0) {
+        tc_ld32(o, o_at + 32 * c);
+        tc_wait_ld(o);
+      } else {
+#pragma unroll
+        for (int e = 0; e < 32; ++e) o[e] = 0u;
+      }
+      if (ok && token >= 0) {
+        if (a.rows_o) {
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            *reinterpret_cast<uint4*>(a.rows_o + at * D + 32 * c + 4 * e) =
+                make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+        } else {
+          uint32_t w[16];
+#pragma unroll
+          for (int e = 0; e < 16; ++e)
+            w[e] = l == 0.f ? 0u : T::pack(__uint_as_float(o[2 * e]) * inv, __uint_as_float(o[2 * e + 1]) * inv);
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            *reinterpret_cast<uint4*>(a.out + row * D + 32 * c + 8 * e) =
+                make_uint4(w[4 * e], w[4 * e + 1], w[4 * e + 2], w[4 * e + 3]);
+        }
+      }
+    }
+    if (ok && token >= 0) {
+      if (a.rows_o)
+        *reinterpret_cast<float2*>(a.rows_ml + 2 * at) = make_float2(m, l);
+      else if (a.lse)
+        a.lse[row] = l == 0.f ? -INFINITY : m * 0.6931471805599453f + logf(l);
+    }
+    tc_fence_before();
+  }
+  __syncthreads();
+  tc_fence_after();
+  if (sh.dead) {
+    // a wait gave up: report it, and let copies still in flight land before
+    // the shared memory goes to another CTA
+    if (tid == 0) {
+      *a.b.status = kDeviceTimeout;
+      const uint64_t t0 = global_timer_ns();
+      while (global_timer_ns() - t0 < 10000000ull) {
+      }
+    }
+    __syncthreads();
+  }
+  if (warp == 1)
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;\n" ::"r"(tmem), "r"(C::COLS));
+}
+
+// Rows whose state lies in parts: slots [0, shared) of every row, then one
+// slot of the decode kernel or `own` slots of the prompt kernel.  One warp a
+// row; the parts of a row are read in order, so results do not depend on
+// timing.
+template <class T, int D>
+__global__ void __launch_bounds__(128) paged_merge_kernel(const __grid_constant__ PagedAttnArgs a, int shared, int own) {
+  const int lane = threadIdx.x & 31;
+  const int64_t row = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5);
+  const int64_t n_rows = (int64_t)a.b.n_tokens * a.b.hq;
+  if (row >= n_rows) return;
+  const int token = (int)(row / a.b.hq);
+  const int b = seq_of(a.b, token);
+  if (b < 0) return;
+  const Seq s = load_seq(a.b, b);
+  if (token < s.t0 || token >= s.t0 + s.n) return;
+  const bool few = a.few_rows_apart && (s.n << a.b.g_shift) <= kDecodeRows;
+  if (few && shared == 0) return;  // the decode kernel wrote the result
+  const int slots = shared + (few ? 1 : own);
+  float M = -INFINITY;
+  for (int k = lane; k < slots; k += 32) M = fmaxf(M, __ldg(a.rows_ml + 2 * (k * n_rows + row)));
+#pragma unroll
+  for (int k = 16; k; k >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, k));
+  const float mu = M == -INFINITY ? 0.f : M;
+  float L = 0.f;
+  constexpr int E = D / 32;
+  float v[E];
+#pragma unroll
+  for (int e = 0; e < E; ++e) v[e] = 0.f;
+#pragma unroll 4
+  for (int k = 0; k < slots; ++k) {
+    const int64_t at = k * n_rows + row;
+    const float2 x = __ldg(reinterpret_cast<const float2*>(a.rows_ml + 2 * at));
+    if (x.x == -INFINITY) continue;
+    const float f = ex2(x.x - mu);
+    L = fmaf(f, x.y, L);
+    if constexpr (E == 4) {
+      const float4 o = __ldg(reinterpret_cast<const float4*>(a.rows_o + at * D) + lane);
+      v[0] = fmaf(f, o.x, v[0]);
+      v[1] = fmaf(f, o.y, v[1]);
+      v[2] = fmaf(f, o.z, v[2]);
+      v[3] = fmaf(f, o.w, v[3]);
+    } else {
+      const float2 o = __ldg(reinterpret_cast<const float2*>(a.rows_o + at * D) + lane);
+      v[0] = fmaf(f, o.x, v[0]);
+      v[1] = fmaf(f, o.y, v[1]);
+    }
+  }
+  const float inv = L == 0.f ? 0.f : 1.f / L;
+  uint32_t* out = reinterpret_cast<uint32_t*>(a.out + row * D) + lane * (E / 2);
+#pragma unroll
+  for (int e = 0; e < E / 2; ++e) out[e] = T::pack(v[2 * e] * inv, v[2 * e + 1] * inv);
+  if (a.lse && lane == 0) a.lse[row] = L == 0.f ? -INFINITY : M * 0.6931471805599453f + logf(L);
+}
+
+template <class T, int D>
+cudaError_t launch(const CUtensorMap& km, const CUtensorMap& vm, const PagedAttnArgs& a, int blocks, int splits,
+                   cudaStream_t s) {
+  static_assert(Cfg<D>::SMEM + sizeof(Shared) + 64 <= 227 * 1024, "shared memory");
+  const cudaError_t e =
+      cudaFuncSetAttribute(paged_prompt_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<D>::SMEM);
+  if (e != cudaSuccess) return e;
+  paged_prompt_kernel<T, D><<<dim3(blocks, a.b.hkv, splits), kThreads, Cfg<D>::SMEM, s>>>(km, vm, a);
+  return cudaGetLastError();
+}
+
+template <class T, int D>
+cudaError_t merge(const PagedAttnArgs& a, int shared, int own, cudaStream_t s) {
+  const int64_t rows = (int64_t)a.b.n_tokens * a.b.hq;
+  paged_merge_kernel<T, D><<<(unsigned)((rows + 3) / 4), 128, 0, s>>>(a, shared, own);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_paged_prompt(const CUtensorMap& km, const CUtensorMap& vm, const PagedAttnArgs& a, int blocks,
+                                int splits, int head_dim, int dtype, cudaStream_t s) {
+  if (head_dim == 128)
+    return dtype == 0 ? launch<Bf16, 128>(km, vm, a, blocks, splits, s) : launch<Fp16, 128>(km, vm, a, blocks, splits, s);
+  return dtype == 0 ? launch<Bf16, 64>(km, vm, a, blocks, splits, s) : launch<Fp16, 64>(km, vm, a, blocks, splits, s);
+}
+
+cudaError_t launch_paged_merge(const PagedAttnArgs& a, int shared, int own, int head_dim, int dtype, cudaStream_t s) {
+  if (head_dim == 128) return dtype == 0 ? merge<Bf16, 128>(a, shared, own, s) : merge<Fp16, 128>(a, shared, own, s);
+  return dtype == 0 ? merge<Bf16, 64>(a, shared, own, s) : merge<Fp16, 64>(a, shared, own, s);
+}
+
+}  // namespace rq
