@@ -9,6 +9,22 @@
 
 namespace rq {
 
+// Bounded wait for a barrier's phase (false after about a second).  The clock
+// is read on every 64th try only: it costs more than a try.
+__device__ __forceinline__ bool bar_wait(uint64_t* bar, uint32_t parity) {
+  uint64_t t0 = 0;
+  for (uint32_t i = 1;; ++i) {
+    if (mbar_try_wait(bar, parity)) return true;
+    if ((i & 63u) == 0) {
+      const uint64_t t = global_timer_ns();
+      if (t0 == 0)
+        t0 = t;
+      else if (t - t0 > kWaitLimitNs)
+        return false;
+    }
+  }
+}
+
 __device__ __forceinline__ void flag_index(int* status) {
   if (status) *status = kDeviceIndex;
 }

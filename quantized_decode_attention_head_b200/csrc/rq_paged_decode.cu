@@ -270,7 +270,7 @@ __global__ void __launch_bounds__(NW * 32, 1)
       const int c = i * NW + warp;
       if (c >= w.chunks) break;
       const int t = chunk_token(w, c);
-      if (!dead && !mbar_wait_bounded(&full[warp][get], phase)) {
+      if (!dead && !bar_wait(&full[warp][get], phase)) {
         dead = true;
         if (lane == 0) *a.b.status = kDeviceTimeout;
       }

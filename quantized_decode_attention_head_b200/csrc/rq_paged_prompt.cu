@@ -53,18 +53,28 @@ __device__ __forceinline__ void tc_commit(uint64_t* bar) {
   asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n" ::"r"(smem_u32(bar))
                : "memory");
 }
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool acc) {
+// One lane of the warp (the same at every call).  With it, and values that are
+// the same in all lanes, the compiler keeps the operands of the MMAs in uniform
+// registers; under a test of the lane number it moves them there before every
+// MMA, which took 130 clocks an MMA instead of 64.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(p));
+  return p != 0;
+}
+// Descriptors come as (low, high) words: only the low one, the address, varies.
+__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a, uint32_t b, uint32_t hi, uint32_t idesc, bool acc) {
   asm volatile(
-      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
-      " tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "r"((int)acc)
+      "{\n .reg .pred p;\n .reg .b64 a, b;\n setp.ne.b32 p, %5, 0;\n mov.b64 a, {%1, %3};\n mov.b64 b, {%2, %3};\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %4, p;\n}\n" ::"r"(d),
+      "r"(a), "r"(b), "r"(hi), "r"(idesc), "r"((int)acc)
       : "memory");
 }
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool acc) {
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b, uint32_t hi, uint32_t idesc, bool acc) {
   asm volatile(
-      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
-      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
-      "r"(a), "l"(b), "r"(idesc), "r"((int)acc)
+      "{\n .reg .pred p;\n .reg .b64 b;\n setp.ne.b32 p, %5, 0;\n mov.b64 b, {%2, %3};\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %4, p;\n}\n" ::"r"(d),
+      "r"(a), "r"(b), "r"(hi), "r"(idesc), "r"((int)acc)
       : "memory");
 }
 
@@ -99,11 +109,10 @@ __device__ __forceinline__ void tc_wait_ld(uint32_t (&r)[32]) {
   asm volatile("tcgen05.wait::ld.sync.aligned;\n" : RQ_32(RQ_TIE)::"memory");
 }
 
-// Shared-memory matrix descriptor: 128-byte swizzle, strides in bytes.
-__device__ __forceinline__ uint64_t smem_desc(uint32_t addr, uint32_t lbo, uint32_t sbo) {
-  return (uint64_t)((addr & 0x3FFFF) >> 4) | (uint64_t)(lbo >> 4) << 16 | (uint64_t)(sbo >> 4) << 32 |
-         (uint64_t)1 << 46 | (uint64_t)2 << 61;
-}
+// Shared-memory matrix descriptor, 128-byte swizzle.  Low word: address and
+// leading stride; high word: stride of 8 rows (1024 bytes), version, swizzle.
+__device__ __forceinline__ uint32_t desc_lo(uint32_t addr, uint32_t lbo) { return (addr >> 4) | (lbo >> 4) << 16; }
+constexpr uint32_t kDescHi = 1024 >> 4 | 1u << 14 | 2u << 29;
 // Instruction descriptor: fp32 accumulator, A and B of the pages' type (0
 // fp16, 1 bf16), B K-major or MN-major.
 __host__ __device__ constexpr uint32_t instr_desc(int type, bool b_mn, int m, int n) {
@@ -119,14 +128,20 @@ __device__ __forceinline__ void tma_box(uint32_t dst, const CUtensorMap* map, in
       : "memory");
 }
 
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;\n" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+
 // A warp's wait: all lanes go on, or none (the tcgen05 accesses need the whole warp).
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity) {
-  return __all_sync(0xffffffffu, mbar_wait_bounded(bar, parity));
+  return __all_sync(0xffffffffu, bar_wait(bar, parity));
 }
 
 struct Shared {
   uint64_t k_full[4], k_empty[4], v_full[4], v_empty[4];
-  uint64_t s_full[2], p_ready[2], o_final[2];
+  uint64_t s_full[2], p_ready[2][2], o_final[2];  // p_ready: halves of a tile's keys
   uint32_t tmem;
   int seq, block;          // the CTA's sequence and row block in it
   int row_token[kBlockRows];  // packed token, -1: no row
@@ -157,7 +172,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   __shared__ Shared sh;
   uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const uint32_t q_sm = smem_u32(sm), k_sm = q_sm + 2 * C::TILE, v_sm = k_sm + C::NS * C::TILE;
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);  // uniform
   const int h = blockIdx.y, G = 1 << a.b.g_shift;
 
   // ---- which rows
@@ -212,7 +228,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int t = 0; t < 2; ++t) {
       mbar_init(&sh.s_full[t], 1);
-      mbar_init(&sh.p_ready[t], kTileRows);
+      mbar_init(&sh.p_ready[t][0], 4);
+      mbar_init(&sh.p_ready[t][1], 4);
       mbar_init(&sh.o_final[t], 1);
     }
     mbar_fence_init();
@@ -261,7 +278,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = sh.tmem;
+  const uint32_t tmem = __shfl_sync(0xffffffffu, sh.tmem, 0);
   int p_lo[2], p_hi[2];
 #pragma unroll
   for (int t = 0; t < 2; ++t) {
@@ -318,6 +335,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   fence_proxy_async_smem();
   const bool any_bad = __syncthreads_or(bad);
 
+  // registers: launched with 168 a thread (64512); 64 + 2 * 216 a lane of the three groups are 63488
+  if (warp < 4) asm volatile("setmaxnreg.dec.sync.aligned.u32 64;\n");
   if (n_steps > 0) {
     if (warp == 0) {
       // ------------------------------------------------ producer
@@ -346,7 +365,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int kv = 0; kv < 2 && ok; ++kv) {
             uint64_t* full = kv ? &sh.v_full[slot] : &sh.k_full[slot];
-            ok = mbar_wait_bounded(kv ? &sh.v_empty[slot] : &sh.k_empty[slot], par);
+            ok = bar_wait(kv ? &sh.v_empty[slot] : &sh.k_empty[slot], par);
             if (!ok) break;
             if (bytes)
               mbar_arrive_expect_tx(full, bytes);
@@ -368,13 +387,16 @@ __global__ void __launch_bounds__(kThreads, 1)
       // ------------------------------------------------ MMA issue
       constexpr uint32_t id_s = instr_desc(T::kType, false, kTileRows, kKeys);
       constexpr uint32_t id_o = instr_desc(T::kType, true, kTileRows, D);
+      const uint32_t q_desc = desc_lo(q_sm, 16), k_desc = desc_lo(k_sm, 16), v_desc = desc_lo(v_sm, C::PANEL);
+      const bool one = elect_one();
       auto scores = [&](int t, int slot) {
-        if (lane == 0) {
+        if (one) {
+          const uint32_t qd = q_desc + t * (C::TILE >> 4), kd = k_desc + slot * (C::TILE >> 4);
 #pragma unroll
           for (int ks = 0; ks < D / 16; ++ks) {
-            const uint32_t off = (ks >> 2) * C::PANEL + (ks & 3) * 32;
-            mma_ss(tmem + t * kKeys, smem_desc(q_sm + t * C::TILE + off, 16, 1024),
-                   smem_desc(k_sm + slot * C::TILE + off, 16, 1024), id_s, ks > 0);
+            constexpr int kPanel16 = C::PANEL >> 4;
+            const uint32_t off = (ks >> 2) * kPanel16 + (ks & 3) * 2;
+            mma_ss(tmem + t * kKeys, qd + off, kd + off, kDescHi, id_s, ks > 0);
           }
           tc_commit(&sh.s_full[t]);
         }
@@ -383,7 +405,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (ok) {
         tc_fence_after();
         for (int t = 0; t < tiles_q; ++t) scores(t, 0);
-        if (lane == 0) tc_commit(&sh.k_empty[0]);
+        if (one) tc_commit(&sh.k_empty[0]);
       }
       for (int k = 0; k < n_steps && ok; ++k) {
         const int slot = k % C::NS, next = (k + 1) % C::NS;
@@ -407,16 +429,21 @@ __global__ void __launch_bounds__(kThreads, 1)
               __syncwarp();
             }
           }
-          ok = ok && warp_wait(&sh.p_ready[t], k & 1);
-          if (!ok) break;
-          tc_fence_after();
-          if (lane == 0) {
 #pragma unroll
-            for (int kt = 0; kt < kKeys / 16; ++kt)
-              mma_ts(tmem + 2 * kKeys + t * D, tmem + t * kKeys + kt * 8,
-                     smem_desc(v_sm + slot * C::TILE + kt * 2048, C::PANEL, 1024), id_o, k > 0 || kt > 0);
-            if (t == tiles_q - 1) tc_commit(&sh.v_empty[slot]);
+          for (int half = 0; half < 2; ++half) {
+            ok = ok && warp_wait(&sh.p_ready[t][half], k & 1);
+            if (!ok) break;
+            tc_fence_after();
+            if (one) {
+              const uint32_t vd = v_desc + slot * (C::TILE >> 4);
+#pragma unroll
+              for (int kt = 4 * half; kt < 4 * half + 4; ++kt)
+                mma_ts(tmem + 2 * kKeys + t * D, tmem + t * kKeys + kt * 8, vd + kt * (2048 >> 4), kDescHi, id_o,
+                       k > 0 || kt > 0);
+            }
           }
+          if (!ok) break;
+          if (t == tiles_q - 1 && one) tc_commit(&sh.v_empty[slot]);
           if (k + 1 < n_steps) {
             if (t == 0) {
               ok = warp_wait(&sh.k_full[next], ((k + 1) / C::NS) & 1);
@@ -424,8 +451,8 @@ __global__ void __launch_bounds__(kThreads, 1)
               tc_fence_after();
             }
             scores(t, next);
-            if (t == tiles_q - 1 && lane == 0) tc_commit(&sh.k_empty[next]);
-          } else if (lane == 0) {
+            if (t == tiles_q - 1 && one) tc_commit(&sh.k_empty[next]);
+          } else if (one) {
             tc_commit(&sh.o_final[t]);
           }
         }
@@ -434,6 +461,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   }
   if (warp >= 4 && (warp - 4) / 4 < tiles_q) {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 216;\n");
     // -------------------------------------------------- softmax, one row a thread
     const int t = (warp - 4) / 4;
     const int r = t * kTileRows + (warp & 3) * 32 + lane;
@@ -457,7 +485,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int c = 0; c < 4; ++c) tc_wait_ld(s[c]);
       const bool whole = !any_bad && j + kKeys <= min(key.end, p_lo[t] + 1 - key.base) &&
                          (a.window == 0 || j > p_hi[t] - a.window - key.base || j + kKeys <= key.sink);
-      if (!whole) {
+      if (__any_sync(0xffffffffu, !whole)) {
         uint32_t pages = 0xFFu;  // bit g: the page of keys 16 g.. of the tile exists
         if (any_bad) {
           pages = 0;
@@ -475,11 +503,15 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (!see) s[c][e] = 0xFF800000u;
           }
       }
-      float mx = -INFINITY;
+      float mx4[4];
 #pragma unroll
-      for (int c = 0; c < 4; ++c)
+      for (int c = 0; c < 4; ++c) {
+        mx4[c] = __uint_as_float(s[c][0]);
 #pragma unroll
-        for (int e = 0; e < 32; ++e) mx = fmaxf(mx, __uint_as_float(s[c][e]));
+        for (int e = 1; e < 31; e += 2) mx4[c] = max3(mx4[c], __uint_as_float(s[c][e]), __uint_as_float(s[c][e + 1]));
+        mx4[c] = fmaxf(mx4[c], __uint_as_float(s[c][31]));
+      }
+      float mx = fmaxf(max3(mx4[0], mx4[1], mx4[2]), mx4[3]);
       mx *= a.scale_log2;
       const bool move = mx > m + 8.0f;  // true at the first score of a row (m = -inf)
       if (__any_sync(0xffffffffu, move)) {
@@ -501,25 +533,38 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       const float mu = m == -INFINITY ? 0.f : m;
-      float sum0 = 0.f, sum1 = 0.f;
+      const float2 sc2 = make_float2(a.scale_log2, a.scale_log2), mu2 = make_float2(-mu, -mu);
+      // weights of 64 keys at a time, so that their product starts while the
+      // other half's are computed
 #pragma unroll
-      for (int c = 0; c < 2; ++c) {
+      for (int half = 0; half < 2; ++half) {
         uint32_t w[32];
 #pragma unroll
         for (int e = 0; e < 32; ++e) {
-          const uint32_t x = s[2 * c + e / 16][2 * (e % 16)], y = s[2 * c + e / 16][2 * (e % 16) + 1];
-          const float px = ex2(fmaf(__uint_as_float(x), a.scale_log2, -mu));
-          const float py = ex2(fmaf(__uint_as_float(y), a.scale_log2, -mu));
-          sum0 += px;
-          sum1 += py;
+          uint32_t &x = s[2 * half + e / 16][2 * (e % 16)], &y = s[2 * half + e / 16][2 * (e % 16) + 1];
+          const float2 d = __ffma2_rn(make_float2(__uint_as_float(x), __uint_as_float(y)), sc2, mu2);
+          const float px = ex2(d.x), py = ex2(d.y);
+          x = __float_as_uint(px);
+          y = __float_as_uint(py);
           w[e] = T::pack(px, py);
         }
-        tc_st32(s_at + 32 * c, w);
+        tc_st32(s_at + 32 * half, w);
+        tc_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh.p_ready[t][half]);
       }
-      l += sum0 + sum1;
-      tc_wait_st();
-      tc_fence_before();
-      mbar_arrive(&sh.p_ready[t]);
+      // the row's sum, off the way to the products
+      float2 sum[4];
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        sum[c] = make_float2(__uint_as_float(s[c][0]), __uint_as_float(s[c][1]));
+#pragma unroll
+        for (int e = 2; e < 32; e += 2)
+          sum[c] = __fadd2_rn(sum[c], make_float2(__uint_as_float(s[c][e]), __uint_as_float(s[c][e + 1])));
+      }
+      const float2 all = __fadd2_rn(__fadd2_rn(sum[0], sum[1]), __fadd2_rn(sum[2], sum[3]));
+      l += all.x + all.y;
     }
     if (ok && n_steps > 0) {
       ok = warp_wait(&sh.o_final[t], 0);
