@@ -31,6 +31,10 @@ constexpr int kTileRows = 128;
 constexpr int kBlockRows = kPromptRows;
 constexpr int kKeys = 128;  // keys a step
 constexpr int kThreads = 384;
+#ifndef RQ_FMA_EVERY
+#define RQ_FMA_EVERY 4
+#endif
+constexpr int kFmaEvery = RQ_FMA_EVERY;
 static_assert(kBlockRows == 2 * kTileRows, "two tiles a CTA");
 
 template <int D>
@@ -133,6 +137,29 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   asm("max.f32 %0, %1, %2, %3;\n" : "=f"(d) : "f"(a), "f"(b), "f"(c));
   return d;
 }
+
+// 2^x of a pair on the FMA pipe: x = n + f with n the nearest integer, a
+// polynomial for 2^f on [-1/2, 1/2] (degree 5, fitted to the least relative
+// error with the constant term 1; 1.7e-7 in fp32), and n added to the exponent.
+// x <= 128; from -127 down the result is 0.
+__device__ __forceinline__ float2 exp2_fma(float2 x) {
+  constexpr float kMagic = 12582912.f;  // 1.5 * 2^23: adding it leaves n in the low bits
+  x = make_float2(fmaxf(x.x, -127.f), fmaxf(x.y, -127.f));
+  const float2 t = __fadd2_rn(x, make_float2(kMagic, kMagic));
+  const float2 n = __fadd2_rn(t, make_float2(-kMagic, -kMagic));
+  const float2 f = __fadd2_rn(x, make_float2(-n.x, -n.y));
+  float2 p = make_float2(1.326472731e-3f, 1.326472731e-3f);
+  p = __ffma2_rn(p, f, make_float2(9.671512991e-3f, 9.671512991e-3f));
+  p = __ffma2_rn(p, f, make_float2(5.550733581e-2f, 5.550733581e-2f));
+  p = __ffma2_rn(p, f, make_float2(2.402224243e-1f, 2.402224243e-1f));
+  p = __ffma2_rn(p, f, make_float2(6.931470037e-1f, 6.931470037e-1f));
+  p = __ffma2_rn(p, f, make_float2(1.f, 1.f));
+  return make_float2(__uint_as_float(__float_as_uint(p.x) + (__float_as_uint(t.x) << 23)),
+                     __uint_as_float(__float_as_uint(p.y) + (__float_as_uint(t.y) << 23)));
+}
+
+// The lowest n bits (n <= 0: none, n >= 32: all).
+__device__ __forceinline__ uint32_t low_bits(int n) { return n >= 32 ? 0xFFFFFFFFu : n <= 0 ? 0u : (1u << n) - 1u; }
 
 // A warp's wait: all lanes go on, or none (the tcgen05 accesses need the whole warp).
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity) {
@@ -470,7 +497,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t s_at = tmem + t * kKeys + lanes, o_at = tmem + 2 * kKeys + t * D + lanes;
     // keys the row sees: [w_lo, limit) and [0, sink), the latter below limit too
     const int limit = token >= 0 ? min(key.end, p + 1 - key.base) : 0;
-    const int w_lo = a.window > 0 ? p + 1 - a.window - key.base : INT_MIN;
+    const int w_lo = a.window > 0 ? p + 1 - a.window - key.base : 0;
     float m = -INFINITY, l = 0.f;
     bool ok = true;
     for (int k = 0; k < n_steps; ++k) {
@@ -495,13 +522,14 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
 #pragma unroll
-        for (int c = 0; c < 4; ++c)
+        for (int c = 0; c < 4; ++c) {
+          // seen: below the limit, and in the window or among the first tokens
+          const int j0 = j + 32 * c;
+          uint32_t see = low_bits(limit - j0) & (~low_bits(w_lo - j0) | low_bits(key.sink - j0));
+          if (any_bad) see &= ((pages >> (2 * c)) & 1u ? 0xFFFFu : 0u) | ((pages >> (2 * c + 1)) & 1u ? 0xFFFF0000u : 0u);
 #pragma unroll
-          for (int e = 0; e < 32; ++e) {
-            const int jj = j + 32 * c + e;
-            const bool see = jj < limit && (jj >= w_lo || jj < key.sink) && ((pages >> (2 * c + e / 16)) & 1u);
-            if (!see) s[c][e] = 0xFF800000u;
-          }
+          for (int e = 0; e < 32; ++e) s[c][e] = (see >> e) & 1u ? s[c][e] : 0xFF800000u;
+        }
       }
       float mx4[4];
 #pragma unroll
@@ -543,10 +571,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int e = 0; e < 32; ++e) {
           uint32_t &x = s[2 * half + e / 16][2 * (e % 16)], &y = s[2 * half + e / 16][2 * (e % 16) + 1];
           const float2 d = __ffma2_rn(make_float2(__uint_as_float(x), __uint_as_float(y)), sc2, mu2);
-          const float px = ex2(d.x), py = ex2(d.y);
-          x = __float_as_uint(px);
-          y = __float_as_uint(py);
-          w[e] = T::pack(px, py);
+          // every kFmaEvery-th pair on the FMA pipe: the special-function
+          // unit alone would need as many clocks as the tensor cores
+          const float2 p = e % kFmaEvery == 0 ? exp2_fma(d) : make_float2(ex2(d.x), ex2(d.y));
+          x = __float_as_uint(p.x);
+          y = __float_as_uint(p.y);
+          w[e] = T::pack(p.x, p.y);
         }
         tc_st32(s_at + 32 * half, w);
         tc_wait_st();
