@@ -31,10 +31,6 @@ constexpr int kTileRows = 128;
 constexpr int kBlockRows = kPromptRows;
 constexpr int kKeys = 128;  // keys a step
 constexpr int kThreads = 384;
-#ifndef RQ_FMA_EVERY
-#define RQ_FMA_EVERY 4
-#endif
-constexpr int kFmaEvery = RQ_FMA_EVERY;
 static_assert(kBlockRows == 2 * kTileRows, "two tiles a CTA");
 
 template <int D>
@@ -52,33 +48,42 @@ __device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence:
 __device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;\n" ::: "memory"); }
 __device__ __forceinline__ void tc_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;\n" ::: "memory"); }
 
-// Arrives on bar when every tcgen05 operation this thread issued before is complete.
-__device__ __forceinline__ void tc_commit(uint64_t* bar) {
-  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n" ::"r"(smem_u32(bar))
-               : "memory");
-}
-// One lane of the warp (the same at every call).  With it, and values that are
-// the same in all lanes, the compiler keeps the operands of the MMAs in uniform
-// registers; under a test of the lane number it moves them there before every
-// MMA, which took 130 clocks an MMA instead of 64.
-__device__ __forceinline__ bool elect_one() {
+// One lane of the warp (the same at every call).  The MMAs and commits below
+// are predicated on it: the flow stays uniform, and with it the compiler keeps
+// descriptors and addresses in uniform registers.  (A 128 x 128 x 16 MMA takes
+// 64 clocks, and issuing blocks after about four; a commit is seen some 300
+// clocks after the last MMA began.)
+__device__ __forceinline__ uint32_t elect_one() {
   uint32_t p;
   asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(p));
-  return p != 0;
+  return p;
 }
-// Descriptors come as (low, high) words: only the low one, the address, varies.
-__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a, uint32_t b, uint32_t hi, uint32_t idesc, bool acc) {
+// Arrives on bar when every tcgen05 operation that the lane issued before is complete.
+__device__ __forceinline__ void tc_commit(uint64_t* bar, uint32_t one) {
   asm volatile(
-      "{\n .reg .pred p;\n .reg .b64 a, b;\n setp.ne.b32 p, %5, 0;\n mov.b64 a, {%1, %3};\n mov.b64 b, {%2, %3};\n"
-      " tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %4, p;\n}\n" ::"r"(d),
-      "r"(a), "r"(b), "r"(hi), "r"(idesc), "r"((int)acc)
+      "{\n .reg .pred q;\n setp.ne.b32 q, %1, 0;\n"
+      " @q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}\n" ::"r"(smem_u32(bar)),
+      "r"(one)
       : "memory");
 }
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b, uint32_t hi, uint32_t idesc, bool acc) {
+// D += A B (D = A B unless acc).  Descriptors come as (low, high) words: only
+// the low one, the address, varies.
+__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a, uint32_t b, uint32_t hi, uint32_t idesc, bool acc,
+                                       uint32_t one) {
   asm volatile(
-      "{\n .reg .pred p;\n .reg .b64 b;\n setp.ne.b32 p, %5, 0;\n mov.b64 b, {%2, %3};\n"
-      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %4, p;\n}\n" ::"r"(d),
-      "r"(a), "r"(b), "r"(hi), "r"(idesc), "r"((int)acc)
+      "{\n .reg .pred p, q;\n .reg .b64 a, b;\n setp.ne.b32 q, %6, 0;\n setp.ne.b32 p, %5, 0;\n"
+      " mov.b64 a, {%1, %3};\n mov.b64 b, {%2, %3};\n"
+      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %4, p;\n}\n" ::"r"(d),
+      "r"(a), "r"(b), "r"(hi), "r"(idesc), "r"((int)acc), "r"(one)
+      : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b, uint32_t hi, uint32_t idesc, bool acc,
+                                       uint32_t one) {
+  asm volatile(
+      "{\n .reg .pred p, q;\n .reg .b64 b;\n setp.ne.b32 q, %6, 0;\n setp.ne.b32 p, %5, 0;\n"
+      " mov.b64 b, {%2, %3};\n"
+      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %4, p;\n}\n" ::"r"(d),
+      "r"(a), "r"(b), "r"(hi), "r"(idesc), "r"((int)acc), "r"(one)
       : "memory");
 }
 
@@ -136,26 +141,6 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   float d;
   asm("max.f32 %0, %1, %2, %3;\n" : "=f"(d) : "f"(a), "f"(b), "f"(c));
   return d;
-}
-
-// 2^x of a pair on the FMA pipe: x = n + f with n the nearest integer, a
-// polynomial for 2^f on [-1/2, 1/2] (degree 5, fitted to the least relative
-// error with the constant term 1; 1.7e-7 in fp32), and n added to the exponent.
-// x <= 128; from -127 down the result is 0.
-__device__ __forceinline__ float2 exp2_fma(float2 x) {
-  constexpr float kMagic = 12582912.f;  // 1.5 * 2^23: adding it leaves n in the low bits
-  x = make_float2(fmaxf(x.x, -127.f), fmaxf(x.y, -127.f));
-  const float2 t = __fadd2_rn(x, make_float2(kMagic, kMagic));
-  const float2 n = __fadd2_rn(t, make_float2(-kMagic, -kMagic));
-  const float2 f = __fadd2_rn(x, make_float2(-n.x, -n.y));
-  float2 p = make_float2(1.326472731e-3f, 1.326472731e-3f);
-  p = __ffma2_rn(p, f, make_float2(9.671512991e-3f, 9.671512991e-3f));
-  p = __ffma2_rn(p, f, make_float2(5.550733581e-2f, 5.550733581e-2f));
-  p = __ffma2_rn(p, f, make_float2(2.402224243e-1f, 2.402224243e-1f));
-  p = __ffma2_rn(p, f, make_float2(6.931470037e-1f, 6.931470037e-1f));
-  p = __ffma2_rn(p, f, make_float2(1.f, 1.f));
-  return make_float2(__uint_as_float(__float_as_uint(p.x) + (__float_as_uint(t.x) << 23)),
-                     __uint_as_float(__float_as_uint(p.y) + (__float_as_uint(t.y) << 23)));
 }
 
 // The lowest n bits (n <= 0: none, n >= 32: all).
@@ -415,24 +400,22 @@ __global__ void __launch_bounds__(kThreads, 1)
       constexpr uint32_t id_s = instr_desc(T::kType, false, kTileRows, kKeys);
       constexpr uint32_t id_o = instr_desc(T::kType, true, kTileRows, D);
       const uint32_t q_desc = desc_lo(q_sm, 16), k_desc = desc_lo(k_sm, 16), v_desc = desc_lo(v_sm, C::PANEL);
-      const bool one = elect_one();
+      const uint32_t one = elect_one();
       auto scores = [&](int t, int slot) {
-        if (one) {
-          const uint32_t qd = q_desc + t * (C::TILE >> 4), kd = k_desc + slot * (C::TILE >> 4);
+        const uint32_t qd = q_desc + t * (C::TILE >> 4), kd = k_desc + slot * (C::TILE >> 4);
 #pragma unroll
-          for (int ks = 0; ks < D / 16; ++ks) {
-            constexpr int kPanel16 = C::PANEL >> 4;
-            const uint32_t off = (ks >> 2) * kPanel16 + (ks & 3) * 2;
-            mma_ss(tmem + t * kKeys, qd + off, kd + off, kDescHi, id_s, ks > 0);
-          }
-          tc_commit(&sh.s_full[t]);
+        for (int ks = 0; ks < D / 16; ++ks) {
+          constexpr int kPanel16 = C::PANEL >> 4;
+          const uint32_t off = (ks >> 2) * kPanel16 + (ks & 3) * 2;
+          mma_ss(tmem + t * kKeys, qd + off, kd + off, kDescHi, id_s, ks > 0, one);
         }
+        tc_commit(&sh.s_full[t], one);
       };
       bool ok = warp_wait(&sh.k_full[0], 0);
       if (ok) {
         tc_fence_after();
         for (int t = 0; t < tiles_q; ++t) scores(t, 0);
-        if (one) tc_commit(&sh.k_empty[0]);
+        tc_commit(&sh.k_empty[0], one);
       }
       for (int k = 0; k < n_steps && ok; ++k) {
         const int slot = k % C::NS, next = (k + 1) % C::NS;
@@ -461,16 +444,14 @@ __global__ void __launch_bounds__(kThreads, 1)
             ok = ok && warp_wait(&sh.p_ready[t][half], k & 1);
             if (!ok) break;
             tc_fence_after();
-            if (one) {
-              const uint32_t vd = v_desc + slot * (C::TILE >> 4);
+            const uint32_t vd = v_desc + slot * (C::TILE >> 4);
 #pragma unroll
-              for (int kt = 4 * half; kt < 4 * half + 4; ++kt)
-                mma_ts(tmem + 2 * kKeys + t * D, tmem + t * kKeys + kt * 8, vd + kt * (2048 >> 4), kDescHi, id_o,
-                       k > 0 || kt > 0);
-            }
+            for (int kt = 4 * half; kt < 4 * half + 4; ++kt)
+              mma_ts(tmem + 2 * kKeys + t * D, tmem + t * kKeys + kt * 8, vd + kt * (2048 >> 4), kDescHi, id_o,
+                     k > 0 || kt > 0, one);
           }
           if (!ok) break;
-          if (t == tiles_q - 1 && one) tc_commit(&sh.v_empty[slot]);
+          if (t == tiles_q - 1) tc_commit(&sh.v_empty[slot], one);
           if (k + 1 < n_steps) {
             if (t == 0) {
               ok = warp_wait(&sh.k_full[next], ((k + 1) / C::NS) & 1);
@@ -478,9 +459,9 @@ __global__ void __launch_bounds__(kThreads, 1)
               tc_fence_after();
             }
             scores(t, next);
-            if (t == tiles_q - 1 && one) tc_commit(&sh.k_empty[next]);
-          } else if (one) {
-            tc_commit(&sh.o_final[t]);
+            if (t == tiles_q - 1) tc_commit(&sh.k_empty[next], one);
+          } else {
+            tc_commit(&sh.o_final[t], one);
           }
         }
       }
@@ -505,14 +486,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       ok = warp_wait(&sh.s_full[t], k & 1);
       if (!ok) break;
       tc_fence_after();
-      uint32_t s[4][32];
-#pragma unroll
-      for (int c = 0; c < 4; ++c) tc_ld32(s[c], s_at + 32 * c);
-#pragma unroll
-      for (int c = 0; c < 4; ++c) tc_wait_ld(s[c]);
       const bool whole = !any_bad && j + kKeys <= min(key.end, p_lo[t] + 1 - key.base) &&
                          (a.window == 0 || j > p_hi[t] - a.window - key.base || j + kKeys <= key.sink);
       if (__any_sync(0xffffffffu, !whole)) {
+        // masked in place, 32 columns at a time: a CTA meets one to three such
+        // tiles, and code unrolled over 128 columns cost more to fetch than to run
         uint32_t pages = 0xFFu;  // bit g: the page of keys 16 g.. of the tile exists
         if (any_bad) {
           pages = 0;
@@ -521,16 +499,26 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (jj < key.end && page_row(a.b, __ldg(key.pages + (jj >> a.b.page_shift))) >= 0) pages |= 1u << g;
           }
         }
-#pragma unroll
+#pragma unroll 1
         for (int c = 0; c < 4; ++c) {
           // seen: below the limit, and in the window or among the first tokens
           const int j0 = j + 32 * c;
           uint32_t see = low_bits(limit - j0) & (~low_bits(w_lo - j0) | low_bits(key.sink - j0));
-          if (any_bad) see &= ((pages >> (2 * c)) & 1u ? 0xFFFFu : 0u) | ((pages >> (2 * c + 1)) & 1u ? 0xFFFF0000u : 0u);
+          see &= ((pages >> (2 * c)) & 1u ? 0xFFFFu : 0u) | ((pages >> (2 * c + 1)) & 1u ? 0xFFFF0000u : 0u);
+          uint32_t x[32];
+          tc_ld32(x, s_at + 32 * c);
+          tc_wait_ld(x);
 #pragma unroll
-          for (int e = 0; e < 32; ++e) s[c][e] = (see >> e) & 1u ? s[c][e] : 0xFF800000u;
+          for (int e = 0; e < 32; ++e) x[e] = (see >> e) & 1u ? x[e] : 0xFF800000u;
+          tc_st32(s_at + 32 * c, x);
         }
+        tc_wait_st();
       }
+      uint32_t s[4][32];
+#pragma unroll
+      for (int c = 0; c < 4; ++c) tc_ld32(s[c], s_at + 32 * c);
+#pragma unroll
+      for (int c = 0; c < 4; ++c) tc_wait_ld(s[c]);
       float mx4[4];
 #pragma unroll
       for (int c = 0; c < 4; ++c) {
@@ -563,27 +551,33 @@ __global__ void __launch_bounds__(kThreads, 1)
       const float mu = m == -INFINITY ? 0.f : m;
       const float2 sc2 = make_float2(a.scale_log2, a.scale_log2), mu2 = make_float2(-mu, -mu);
       // weights of 64 keys at a time, so that their product starts while the
-      // other half's are computed
-#pragma unroll
-      for (int half = 0; half < 2; ++half) {
-        uint32_t w[32];
-#pragma unroll
-        for (int e = 0; e < 32; ++e) {
-          uint32_t &x = s[2 * half + e / 16][2 * (e % 16)], &y = s[2 * half + e / 16][2 * (e % 16) + 1];
-          const float2 d = __ffma2_rn(make_float2(__uint_as_float(x), __uint_as_float(y)), sc2, mu2);
-          // every kFmaEvery-th pair on the FMA pipe: the special-function
-          // unit alone would need as many clocks as the tensor cores
-          const float2 p = e % kFmaEvery == 0 ? exp2_fma(d) : make_float2(ex2(d.x), ex2(d.y));
-          x = __float_as_uint(p.x);
-          y = __float_as_uint(p.y);
-          w[e] = T::pack(p.x, p.y);
-        }
-        tc_st32(s_at + 32 * half, w);
+      // other half's are computed; the first half's store completes under the
+      // first weights of the second
+      auto weights = [&](int half, int e, uint32_t(&w)[32]) {
+        uint32_t &x = s[2 * half + e / 16][2 * (e % 16)], &y = s[2 * half + e / 16][2 * (e % 16) + 1];
+        const float2 d = __ffma2_rn(make_float2(__uint_as_float(x), __uint_as_float(y)), sc2, mu2);
+        const float2 p = make_float2(ex2(d.x), ex2(d.y));
+        x = __float_as_uint(p.x);
+        y = __float_as_uint(p.y);
+        w[e] = T::pack(p.x, p.y);
+      };
+      auto hand_over = [&](int half) {
         tc_wait_st();
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&sh.p_ready[t][half]);
-      }
+      };
+      uint32_t w0[32], w1[32];
+#pragma unroll
+      for (int e = 0; e < 32; ++e) weights(0, e, w0);
+      tc_st32(s_at, w0);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) weights(1, e, w1);
+      hand_over(0);
+#pragma unroll
+      for (int e = 8; e < 32; ++e) weights(1, e, w1);
+      tc_st32(s_at + 32, w1);
+      hand_over(1);
       // the row's sum, off the way to the products
       float2 sum[4];
 #pragma unroll
