@@ -55,6 +55,7 @@ struct PagedAttnArgs {
   int n_sink;
   const int* prefix;      // pages of the shared prefix, or null
   int prefix_len;
+  int first;              // first kernel of the call (see rq_paged_launch.h)
   int over_prefix;        // prompt kernel: all rows of the batch over the prefix
   int few_rows_apart;     // sequences of at most kDecodeRows rows are the decode kernel's
   int few_rows_only;      // the call said that no sequence has more than 16 rows a kv head

@@ -8,6 +8,7 @@
 // block takes one token, its items one after another, so that neighbouring
 // threads move neighbouring vectors.
 #include "rq_paged.cuh"
+#include "rq_paged_launch.h"
 
 namespace rq {
 namespace {
@@ -34,6 +35,8 @@ __device__ __forceinline__ int pair_position(const PagedAppendArgs& a, const int
 
 template <class T, int D>
 __global__ void __launch_bounds__(kThreads) paged_append_kernel(const __grid_constant__ PagedAppendArgs a) {
+  griddep_wait();
+  griddep_launch_dependents();
   const int t = blockIdx.x;
   const int seq = seq_of(a.b, t);
   if (seq < 0) return;
@@ -135,11 +138,8 @@ __global__ void __launch_bounds__(kThreads) paged_append_kernel(const __grid_con
 template <class T>
 cudaError_t launch(const PagedAppendArgs& a, int head_dim, cudaStream_t s) {
   const dim3 grid(a.b.n_tokens, 1);
-  if (head_dim == 128)
-    paged_append_kernel<T, 128><<<grid, kThreads, 0, s>>>(a);
-  else
-    paged_append_kernel<T, 64><<<grid, kThreads, 0, s>>>(a);
-  return cudaGetLastError();
+  return head_dim == 128 ? launch_pdl<paged_append_kernel<T, 128>>(grid, kThreads, 0, s, a)
+                         : launch_pdl<paged_append_kernel<T, 64>>(grid, kThreads, 0, s, a);
 }
 
 }  // namespace

@@ -23,6 +23,7 @@
 #include <cuda.h>
 
 #include "rq_paged.cuh"
+#include "rq_paged_launch.h"
 
 namespace rq {
 namespace {
@@ -52,7 +53,8 @@ struct Walk {
   int ns, lo_c, chunks, units;
 };
 __device__ __forceinline__ Walk walk_of(const PagedAttnArgs& a, int b) {
-  Walk w;
+  Walk w = {};
+  if (b >= a.b.n_seqs) return w;  // no units
   const Seq s = load_seq(a.b, b);
   w.t0 = s.t0;
   w.n = s.n;
@@ -84,9 +86,7 @@ struct Cursor {
     if (++h < a.b.hkv) return;
     h = 0;
     do {
-      ++b;
-      w.units = 0;
-      if (b < a.b.n_seqs) w = walk_of(a, b);
+      w = walk_of(a, ++b);
     } while (b < a.b.n_seqs && w.units == 0);
   }
 };
@@ -119,59 +119,85 @@ __global__ void __launch_bounds__(NW * 32, 1)
   __shared__ uint64_t full[NW][C::S];
   __shared__ uint32_t pages_ok[NW][C::S];  // bit k: the page of tokens 16 k.. of the chunk exists
   __shared__ float ml[NW][kRows][2];
-  __shared__ int64_t sh64[NW + 2];
+  __shared__ int64_t sh64[2 * NW + 1];
   __shared__ int sh32[2];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int gid = lane >> 2, tig = lane & 3;
 
-  // ---- the line of units: its length, and where this CTA's share begins
-  int64_t mine = 0;
-  for (int b = tid; b < a.b.n_seqs; b += NW * 32) mine += walk_of(a, b).units;
-#pragma unroll
-  for (int k = 16; k; k >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, k);
-  if (lane == 0) sh64[warp] = mine;
   if (tid < NW * C::S) mbar_init(&full[tid / C::S][tid % C::S], 1);
   mbar_fence_init();
+  // the first kernel of a call, or after another of the same call: nothing
+  // that one writes is read here
+  if (a.first) griddep_wait();
+  griddep_launch_dependents();
+
+  // ---- the line of units: its length, and where this CTA's share begins
+  const Walk w0 = walk_of(a, tid);  // of sequence tid: all there is in batches up to 128
+  int64_t scan = w0.units;          // inclusive over the sequences of the block
+#pragma unroll
+  for (int k = 1; k < 32; k <<= 1) {
+    const int64_t y = __shfl_up_sync(0xffffffffu, scan, k);
+    if (lane >= k) scan += y;
+  }
+  int64_t more = 0;
+  for (int b = tid + NW * 32; b < a.b.n_seqs; b += NW * 32) more += walk_of(a, b).units;
+#pragma unroll
+  for (int k = 16; k; k >>= 1) more += __shfl_xor_sync(0xffffffffu, more, k);
+  if (lane == 31) {
+    sh64[warp] = scan;
+    sh64[NW + warp] = more;
+  }
   __syncthreads();
-  const int64_t U = (sh64[0] + sh64[1] + sh64[2] + sh64[3]) * a.b.hkv;
+  int64_t block = 0;
+  more = 0;
+#pragma unroll
+  for (int k = 0; k < NW; ++k) {
+    if (k < warp) scan += sh64[k];
+    block += sh64[k];
+    more += sh64[NW + k];
+  }
+  const int64_t U = (block + more) * a.b.hkv;
   const int64_t N = U < (int64_t)gridDim.x ? U : (int64_t)gridDim.x;
   const int cta = blockIdx.x;
-  if (cta >= N) return;
+  if (cta >= N) {
+    griddep_wait();
+    return;
+  }
   const int64_t u0 = share_begin(cta, U, N), u1 = share_begin(cta + 1, U, N);
-  __syncthreads();
   Cursor cur;
-  int64_t base = 0;  // first unit of the current sequence
+  int64_t base;  // first unit of the current sequence
   {
-    const int64_t want = u0 / a.b.hkv;  // in units of all heads: sequences take units * hkv each
+    const int64_t want = u0 / a.b.hkv;  // in units of one head: sequence b takes units * hkv
     int64_t before = 0;
-    for (int b0 = 0;; b0 += NW * 32) {
+    int64_t v = w0.units;
+    for (int b0 = 0;;) {
+      if (want >= before + scan - v && want < before + scan) {
+        sh32[0] = b0 + tid;
+        sh64[2 * NW] = before + scan - v;
+      }
+      __syncthreads();
+      if (want < before + block) break;
+      before += block;
+      b0 += NW * 32;
       if (b0 >= a.b.n_seqs) return;  // the lengths changed under the call
-      const int b = b0 + tid;
-      int64_t v = b < a.b.n_seqs ? walk_of(a, b).units : 0, x = v;
+      scan = v = walk_of(a, b0 + tid).units;
 #pragma unroll
       for (int k = 1; k < 32; k <<= 1) {
-        const int64_t y = __shfl_up_sync(0xffffffffu, x, k);
-        if (lane >= k) x += y;
+        const int64_t y = __shfl_up_sync(0xffffffffu, scan, k);
+        if (lane >= k) scan += y;
       }
-      if (lane == 31) sh64[warp] = x;
+      if (lane == 31) sh64[warp] = scan;
       __syncthreads();
-      int64_t sum = 0;
+      block = 0;
 #pragma unroll
       for (int k = 0; k < NW; ++k) {
-        if (k < warp) x += sh64[k];
-        sum += sh64[k];
+        if (k < warp) scan += sh64[k];
+        block += sh64[k];
       }
-      if (want >= before + x - v && want < before + x) {
-        sh32[0] = b;
-        sh64[NW] = before + x - v;
-      }
-      const bool found = want < before + sum;
       __syncthreads();
-      if (found) break;
-      before += sum;
     }
     cur.b = sh32[0];
-    base = sh64[NW] * a.b.hkv;
+    base = sh64[2 * NW] * a.b.hkv;
     cur.w = walk_of(a, cur.b);
     const int64_t rem = u0 - base;
     cur.h = (int)(rem / cur.w.units);
@@ -486,6 +512,7 @@ __global__ void __launch_bounds__(NW * 32, 1)
       if (cur.b != b) base += seq_units;
     }
   }
+  if (!a.first) griddep_wait();
 }
 
 template <class T, int D>
@@ -493,11 +520,7 @@ cudaError_t launch(const CUtensorMap& km, const CUtensorMap& vm, const PagedAttn
   static_assert(Cfg<D>::SMEM <= 227 * 1024 - 1024, "shared memory");
   static_assert(Cfg<D>::MERGE >= kRows * kMaxParts * 4, "weights of the last merge fit the merge buffer");
   static_assert(NW * Cfg<D>::S <= NW * 32, "one thread initialises each barrier");
-  const cudaError_t e =
-      cudaFuncSetAttribute(paged_decode_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<D>::SMEM);
-  if (e != cudaSuccess) return e;
-  paged_decode_kernel<T, D><<<a.n_ctas, NW * 32, Cfg<D>::SMEM, s>>>(km, vm, a);
-  return cudaGetLastError();
+  return launch_pdl<paged_decode_kernel<T, D>>(dim3(a.n_ctas), NW * 32, Cfg<D>::SMEM, s, km, vm, a);
 }
 
 }  // namespace

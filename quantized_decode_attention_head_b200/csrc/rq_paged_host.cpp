@@ -59,7 +59,8 @@ rq_status fill_batch(const rq_paged_cache* c, int layer, const rq_paged_batch* b
 
 bool good_stride(int64_t stride, int heads, int d) { return stride >= (int64_t)heads * d && stride % 8 == 0; }
 
-// Workspace: status word, counters, the decode kernel's partial states.  The
+// Workspace: status word at its start, then, from the next multiple of 256
+// bytes that leaves room for it: counters, the decode kernel's partial states.  The
 // offsets do not depend on the batch, so calls of different batches may share
 // a workspace one after another.
 constexpr size_t kStatusBytes = 256;
@@ -158,8 +159,9 @@ rq_status attention(rq_paged_cache* c, int layer, const rq_paged_batch* batch, c
   const rq_status pr = prepare(c);
   if (pr != RQ_OK) return pr;
   uint8_t* ws = static_cast<uint8_t*>(workspace);
-  a.counters = reinterpret_cast<uint32_t*>(ws + kStatusBytes);
-  a.parts = reinterpret_cast<float*>(ws + kStatusBytes + kCounterBytes);
+  uint8_t* body = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(ws) + 2 * kStatusBytes - 1) / kStatusBytes * kStatusBytes);
+  a.counters = reinterpret_cast<uint32_t*>(body);
+  a.parts = reinterpret_cast<float*>(body + kCounterBytes);
   a.rows_o = a.rows_ml = nullptr;
   a.row_slot = a.over_prefix = 0;
   a.n_ctas = decode_ctas(c);
@@ -199,18 +201,21 @@ rq_status attention(rq_paged_cache* c, int layer, const rq_paged_batch* batch, c
   if (blocks > 0x7FFFFFFF || shared_blocks > 0x7FFFFFFF) return RQ_ERR_UNSUPPORTED;
   const bool merge = shared > 0 || own > 1;
   if (merge) {
-    a.rows_o = reinterpret_cast<float*>(ws + kStatusBytes + kCounterBytes + parts_bytes(c));
+    a.rows_o = reinterpret_cast<float*>(body + kCounterBytes + parts_bytes(c));
     a.rows_ml = a.rows_o + 2 * part_rows(c, batch->n_tokens) * d;
   }
   cudaError_t e = cudaSuccess;
+  a.first = 1;
   if (shared > 0) {
     a.over_prefix = 1;
     e = rq::launch_paged_prompt(c->kp, c->vp, a, (int)shared_blocks, shared, d, type, stream);
-    a.over_prefix = 0;
+    a.over_prefix = a.first = 0;
     a.row_slot = shared;
   }
-  if (e == cudaSuccess && prompt && blocks > 0)
+  if (e == cudaSuccess && prompt && blocks > 0) {
     e = rq::launch_paged_prompt(c->kp, c->vp, a, (int)blocks, own, d, type, stream);
+    a.first = 0;
+  }
   if (e == cudaSuccess && decode) {
     rq::PagedAttnArgs f = a;
     if (shared == 0) f.rows_o = f.rows_ml = nullptr;  // straight to out
@@ -301,7 +306,7 @@ rq_status rq_paged_append(rq_paged_cache* c, int layer, const rq_paged_batch* ba
 rq_status rq_paged_workspace_bytes(const rq_paged_cache* c, int n_seqs, int n_tokens, size_t* bytes) {
   if (!c || !bytes || n_seqs < 0 || n_tokens < 0) return RQ_ERR_INVALID_ARG;
   // the shared prefix and what follows it are one pass each
-  *bytes = kStatusBytes + kCounterBytes + parts_bytes(c) +
+  *bytes = 2 * kStatusBytes + kCounterBytes + parts_bytes(c) +
            (size_t)(2 * part_rows(c, n_tokens)) * (c->cfg.head_dim + 2) * 4;
   return RQ_OK;
 }

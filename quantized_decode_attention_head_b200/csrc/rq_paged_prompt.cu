@@ -23,6 +23,7 @@
 #include <climits>
 
 #include "rq_paged.cuh"
+#include "rq_paged_launch.h"
 
 namespace rq {
 namespace {
@@ -151,6 +152,16 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity) {
   return __all_sync(0xffffffffu, bar_wait(bar, parity));
 }
 
+// Barrier of the MMA warp and the softmax warps.
+__device__ __forceinline__ void named_barrier() { asm volatile("bar.sync 1, 288;\n" ::: "memory"); }
+
+// Eight words to a 32-byte boundary.
+__device__ __forceinline__ void st_v8(void* p, const uint32_t* r) {
+  asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};\n" ::"l"(p), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]),
+               "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
+}
+
 struct Shared {
   uint64_t k_full[4], k_empty[4], v_full[4], v_empty[4];
   uint64_t s_full[2], p_ready[2][2], o_final[2];  // p_ready: halves of a tile's keys
@@ -160,6 +171,7 @@ struct Shared {
   int row_p[kBlockRows];      // position of the row's query
   int p_min[8], p_max[8];     // of each warp's 32 rows
   int dead;
+  int bad;  // a page number out of range in the CTA's walk
 };
 
 // The keys a CTA walks over, as tokens of its page list: tiles [0, ns) and
@@ -187,6 +199,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int tid = threadIdx.x, lane = tid & 31;
   const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);  // uniform
   const int h = blockIdx.y, G = 1 << a.b.g_shift;
+
+  // the first kernel of a call, or after another of the same call: nothing
+  // that one writes is read here before it ends
+  if (a.first) griddep_wait();
+  griddep_launch_dependents();
 
   // ---- which rows
   int row0 = 0, rows = 0;
@@ -226,7 +243,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
     __syncthreads();
-    if (sh.seq < 0) return;
+    if (sh.seq < 0) {
+      griddep_wait();
+      return;
+    }
     seq = load_seq(a.b, sh.seq);
     row0 = sh.block * kBlockRows;
     rows = seq.n << a.b.g_shift;
@@ -246,6 +266,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     mbar_fence_init();
     sh.dead = 0;
+    sh.bad = 0;
   }
   if (warp == 1) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;\n" ::"r"(smem_u32(&sh.tmem)),
@@ -323,30 +344,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   const int n_steps = key.t1 - key.t0;
 
-  // ---- page numbers out of range anywhere in the walk: the masked path
-  bool bad = false;
-  {
-    const int per = kKeys >> a.b.page_shift;  // pages a tile
-    for (int i = tid; i < n_steps * per; i += kThreads) {
-      const int j = key_of(key, key.t0 + i / per) + ((i % per) << a.b.page_shift);
-      if (j < key.end && page_row(a.b, __ldg(key.pages + (j >> a.b.page_shift))) < 0) bad = true;
-    }
-  }
-
-  // ---- queries to shared memory, in the layout a TMA copy would give them
-  for (int i = tid; i < tiles_q * kTileRows * (D / 8); i += kThreads) {
-    const int r = i / (D / 8), c = i % (D / 8);
-    const int token = sh.row_token[r];
-    uint4 x = make_uint4(0, 0, 0, 0);
-    if (token >= 0)
-      x = __ldg(reinterpret_cast<const uint4*>(a.q + token * a.q_stride + (h * G + ((row0 + r) & (G - 1))) * D) + c);
-    const int rr = r & (kTileRows - 1);
-    *reinterpret_cast<uint4*>(sm + (r / kTileRows) * C::TILE + (c >> 3) * C::PANEL + rr * 128 +
-                              (((c & 7) ^ (rr & 7)) << 4)) = x;
-  }
-  fence_proxy_async_smem();
-  const bool any_bad = __syncthreads_or(bad);
-
   // registers: launched with 168 a thread (64512); 64 + 2 * 216 a lane of the three groups are 63488
   if (warp < 4) asm volatile("setmaxnreg.dec.sync.aligned.u32 64;\n");
   if (n_steps > 0) {
@@ -401,6 +398,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       constexpr uint32_t id_o = instr_desc(T::kType, true, kTileRows, D);
       const uint32_t q_desc = desc_lo(q_sm, 16), k_desc = desc_lo(k_sm, 16), v_desc = desc_lo(v_sm, C::PANEL);
       const uint32_t one = elect_one();
+      named_barrier();  // the queries are in shared memory
+      const bool any_bad = sh.bad != 0;
       auto scores = [&](int t, int slot) {
         const uint32_t qd = q_desc + t * (C::TILE >> 4), kd = k_desc + slot * (C::TILE >> 4);
 #pragma unroll
@@ -468,7 +467,40 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!ok && lane == 0) sh.dead = 1;
     }
   }
+  if (warp >= 4 && n_steps > 0) {
+    // ---- queries to shared memory, in the layout a TMA copy would give them:
+    // each warp the 32 rows whose softmax it does, all loads in flight at once
+    constexpr int kVec = D / 8, kRowsAt = 32 / kVec, kLoads = 32 / kRowsAt;  // 16-byte vectors of a row, rows a load
+    const int r0 = (warp - 4) * 32;
+    if (r0 < tiles_q * kTileRows) {
+      uint4 x[kLoads];
+      const int c = lane % kVec;
+#pragma unroll
+      for (int i = 0; i < kLoads; ++i) {
+        const int r = r0 + i * kRowsAt + lane / kVec;
+        const int token = sh.row_token[r];
+        x[i] = make_uint4(0, 0, 0, 0);
+        if (token >= 0)
+          x[i] = __ldg(reinterpret_cast<const uint4*>(a.q + token * a.q_stride + (h * G + ((row0 + r) & (G - 1))) * D) + c);
+      }
+#pragma unroll
+      for (int i = 0; i < kLoads; ++i) {
+        const int r = r0 + i * kRowsAt + lane / kVec, rr = r & (kTileRows - 1);
+        *reinterpret_cast<uint4*>(sm + (r / kTileRows) * C::TILE + (c >> 3) * C::PANEL + rr * 128 +
+                                  (((c & 7) ^ (rr & 7)) << 4)) = x[i];
+      }
+    }
+    // ---- page numbers out of range anywhere in the walk: the masked path
+    const int per = kKeys >> a.b.page_shift;  // pages a tile
+    for (int i = tid - 128; i < n_steps * per; i += 256) {
+      const int j = key_of(key, key.t0 + i / per) + ((i % per) << a.b.page_shift);
+      if (j < key.end && page_row(a.b, __ldg(key.pages + (j >> a.b.page_shift))) < 0) sh.bad = 1;
+    }
+    fence_proxy_async_smem();
+    named_barrier();
+  }
   if (warp >= 4 && (warp - 4) / 4 < tiles_q) {
+    const bool any_bad = sh.bad != 0;
     asm volatile("setmaxnreg.inc.sync.aligned.u32 216;\n");
     // -------------------------------------------------- softmax, one row a thread
     const int t = (warp - 4) / 4;
@@ -611,9 +643,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (ok && token >= 0) {
         if (a.rows_o) {
 #pragma unroll
-          for (int e = 0; e < 8; ++e)
-            *reinterpret_cast<uint4*>(a.rows_o + at * D + 32 * c + 4 * e) =
-                make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+          for (int e = 0; e < 4; ++e) st_v8(a.rows_o + at * D + 32 * c + 8 * e, o + 8 * e);
         } else {
           uint32_t w[16];
 #pragma unroll
@@ -647,6 +677,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     __syncthreads();
   }
+  if (!a.first) griddep_wait();
   if (warp == 1)
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;\n" ::"r"(tmem), "r"(C::COLS));
 }
@@ -660,6 +691,8 @@ __global__ void __launch_bounds__(128) paged_merge_kernel(const __grid_constant_
   const int lane = threadIdx.x & 31;
   const int64_t row = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5);
   const int64_t n_rows = (int64_t)a.b.n_tokens * a.b.hq;
+  griddep_wait();
+  griddep_launch_dependents();
   if (row >= n_rows) return;
   const int token = (int)(row / a.b.hq);
   const int b = seq_of(a.b, token);
@@ -679,11 +712,11 @@ __global__ void __launch_bounds__(128) paged_merge_kernel(const __grid_constant_
   float v[E];
 #pragma unroll
   for (int e = 0; e < E; ++e) v[e] = 0.f;
-#pragma unroll 4
+  // (a part that saw nothing holds zeros and the maximum -inf: weight 0)
+#pragma unroll 8
   for (int k = 0; k < slots; ++k) {
     const int64_t at = k * n_rows + row;
     const float2 x = __ldg(reinterpret_cast<const float2*>(a.rows_ml + 2 * at));
-    if (x.x == -INFINITY) continue;
     const float f = ex2(x.x - mu);
     L = fmaf(f, x.y, L);
     if constexpr (E == 4) {
@@ -709,18 +742,13 @@ template <class T, int D>
 cudaError_t launch(const CUtensorMap& km, const CUtensorMap& vm, const PagedAttnArgs& a, int blocks, int splits,
                    cudaStream_t s) {
   static_assert(Cfg<D>::SMEM + sizeof(Shared) + 64 <= 227 * 1024, "shared memory");
-  const cudaError_t e =
-      cudaFuncSetAttribute(paged_prompt_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<D>::SMEM);
-  if (e != cudaSuccess) return e;
-  paged_prompt_kernel<T, D><<<dim3(blocks, a.b.hkv, splits), kThreads, Cfg<D>::SMEM, s>>>(km, vm, a);
-  return cudaGetLastError();
+  return launch_pdl<paged_prompt_kernel<T, D>>(dim3(blocks, a.b.hkv, splits), kThreads, Cfg<D>::SMEM, s, km, vm, a);
 }
 
 template <class T, int D>
 cudaError_t merge(const PagedAttnArgs& a, int shared, int own, cudaStream_t s) {
   const int64_t rows = (int64_t)a.b.n_tokens * a.b.hq;
-  paged_merge_kernel<T, D><<<(unsigned)((rows + 3) / 4), 128, 0, s>>>(a, shared, own);
-  return cudaGetLastError();
+  return launch_pdl<paged_merge_kernel<T, D>>(dim3((unsigned)((rows + 3) / 4)), 128, 0, s, a, shared, own);
 }
 
 }  // namespace
