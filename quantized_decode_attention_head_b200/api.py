@@ -297,6 +297,9 @@ class PagedKVCache:
     each sequence, new ones included.  cu_new: int32 [n_seqs + 1], where each
     sequence's new tokens begin among the packed ones; None: one new token
     each.  All three are CUDA tensors, read when the kernel runs.
+
+    Calls run on `stream`, or on the current stream of the pages' device.  As
+    the C handle, an object is for one thread of control.
     """
 
     def __init__(self, k_pages, v_pages, n_q_heads):
@@ -324,6 +327,16 @@ class PagedKVCache:
             self.append_status = torch.zeros(1, dtype=torch.int32, device=k_pages.device)
         self.handle = handle
         self._destroy = lib().rq_paged_cache_destroy
+        # the structures that calls fill in, and what a call needs of torch
+        self._b, self._r = PagedBatch(), Rotation()
+        self._b_ref, self._r_ref = ctypes.byref(self._b), ctypes.byref(self._r)
+        self._status_ptr = self.append_status.data_ptr()
+        self._i32, self._f32, self._empty_like = torch.int32, torch.float32, torch.empty_like
+        self._contiguous = torch.contiguous_format
+        self._device_guard = torch.cuda.device
+        self._append_fn = lib().rq_paged_append
+        self._attention_fns = lib().rq_paged_attention, lib().rq_paged_shared_attention
+        self._raw_stream, self._current = torch._C._cuda_getCurrentRawStream, torch.cuda.current_device
 
     def __del__(self):
         h = getattr(self, "handle", None)
@@ -333,43 +346,47 @@ class PagedKVCache:
             self.handle = None
 
     # -- arguments -----------------------------------------------------------
-    def _batch(self, n_tokens, page_table, kv_lens, cu_new, max_new):
-        import torch
+    def _ints(self, name, t, shape):
+        """Address of an int32 tensor of the pages' device."""
+        # one cheap test on the common path; the detailed message only on failure
+        if t.dtype is self._i32 and t.get_device() == self.device and t.shape == shape and t.is_contiguous():
+            return t.data_ptr()
+        _check_tensor(name, t, self._i32, shape, align=4)
+        _same_device(name, t, self.device)
+        return t.data_ptr()
 
-        if not isinstance(page_table, torch.Tensor) or page_table.dim() != 2 or page_table.shape[1] < 1:
+    def _batch(self, n_tokens, page_table, kv_lens, cu_new, max_new):
+        """Fills the batch structure in; returns the number of sequences."""
+        if page_table.dim() != 2 or page_table.shape[1] < 1:
             raise ValueError("page_table must be a tensor [n_seqs, width], width >= 1")
-        n_seqs, width = page_table.shape
-        _check_tensor("page_table", page_table, torch.int32, align=4)
-        _check_tensor("kv_lens", kv_lens, torch.int32, (n_seqs,), align=4)
-        _same_device("page_table", page_table, self.device)
-        _same_device("kv_lens", kv_lens, self.device)
+        shape = page_table.shape
+        n_seqs, b = shape[0], self._b
+        b.n_seqs, b.table_width = shape
+        b.n_tokens = n_tokens
+        b.page_table = self._ints("page_table", page_table, shape)
+        b.kv_lens = self._ints("kv_lens", kv_lens, (n_seqs,))
         if cu_new is None:
             if n_tokens < n_seqs:
                 raise ValueError(f"{n_tokens} packed tokens for {n_seqs} sequences of one new token each")
-            cu, max_new = None, 1
+            b.cu_new, b.max_new = None, 1
         else:
-            _check_tensor("cu_new", cu_new, torch.int32, (n_seqs + 1,), align=4)
-            _same_device("cu_new", cu_new, self.device)
-            cu = cu_new.data_ptr()
-            max_new = n_tokens if max_new is None else int(max_new)
-        return PagedBatch(n_seqs, n_tokens, max_new, width, page_table.data_ptr(), kv_lens.data_ptr(), cu)
+            b.cu_new = self._ints("cu_new", cu_new, (n_seqs + 1,))
+            b.max_new = n_tokens if max_new is None else max_new
+        return n_seqs
 
     def _packed(self, name, t, heads):
         """Tokens of `heads` contiguous heads each; the tokens may lie apart
         (a part of a wider tensor).  Returns the elements between tokens."""
-        import torch
-
         d = self.head_dim
-        if not isinstance(t, torch.Tensor):
-            raise TypeError(f"{name} must be a torch.Tensor")
         if t.dtype is not self.dtype:
             raise TypeError(f"{name} must be {self.dtype}, got {t.dtype}")
         if t.get_device() != self.device:
             raise ValueError(f"{name} must be on the device of the pages")
-        if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != d:
-            raise ValueError(f"{name} has shape {tuple(t.shape)}, expected (tokens, {heads}, {d})")
+        shape = t.shape
+        if len(shape) != 3 or shape[1] != heads or shape[2] != d:
+            raise ValueError(f"{name} has shape {tuple(shape)}, expected (tokens, {heads}, {d})")
         s0, s1, s2 = t.stride()
-        if t.shape[0] <= 1:
+        if shape[0] <= 1:
             s0 = heads * d
         if s2 != 1 or (s1 != d and heads > 1) or s0 < heads * d or s0 % 8:
             raise ValueError(f"{name}: a token's heads must be contiguous and tokens lie a multiple of 8 elements apart")
@@ -377,16 +394,16 @@ class PagedKVCache:
             raise ValueError(f"{name} must start on a 16-byte boundary (a view at an offset into a larger tensor?)")
         return s0
 
-    def _launch(self, func, stream, *args):
-        """Calls func on `stream` (default: the current stream of the pages'
+    def _launch(self, func, fn, stream, *args):
+        """Calls fn on `stream` (default: the current stream of the pages'
         device), with that device current."""
-        import torch
-
-        if stream is None and torch.cuda.current_device() == self.device:
-            check(func, getattr(lib(), func)(*args, torch._C._cuda_getCurrentRawStream(self.device)))
-            return
-        with torch.cuda.device(self.device):
-            check(func, getattr(lib(), func)(*args, _stream_ptr(stream, self.device)))
+        if self._current() == self.device:
+            code = fn(*args, self._raw_stream(self.device) if stream is None else stream.cuda_stream)
+        else:
+            with self._device_guard(self.device):
+                code = fn(*args, self._raw_stream(self.device) if stream is None else stream.cuda_stream)
+        if code:
+            check(func, code)
 
     # -- calls ---------------------------------------------------------------
     def rq_paged_append(self, layer, k_new, v_new, page_table, kv_lens, cu_new=None, q=None, q_out=None, cos_sin=None,
@@ -400,53 +417,51 @@ class PagedKVCache:
         channel pairs turn by each axis; None: a token's place in its
         sequence.  interleaved: channels 2j, 2j + 1 are a pair (else j and
         j + rot_dim/2)."""
-        import torch
-
         ks = self._packed("k_new", k_new, self.n_kv_heads)
         vs = self._packed("v_new", v_new, self.n_kv_heads)
         n = k_new.shape[0]
         if v_new.shape[0] != n:
             raise ValueError(f"v_new has {v_new.shape[0]} tokens, k_new {n}")
-        batch = self._batch(n, page_table, kv_lens, cu_new, None)
+        self._batch(n, page_table, kv_lens, cu_new, None)
         rot, qs, q_ptr, out_ptr = None, 0, None, None
         if cos_sin is None:
             if q is not None or positions is not None or sections is not None:
                 raise ValueError("q, positions and sections go with cos_sin")
         else:
-            if not isinstance(cos_sin, torch.Tensor) or cos_sin.dim() != 2:
+            if cos_sin.dim() != 2:
                 raise ValueError("cos_sin must be a tensor [n_positions, rot_dim]")
-            _check_tensor("cos_sin", cos_sin, torch.float32)
+            _check_tensor("cos_sin", cos_sin, self._f32)
             _same_device("cos_sin", cos_sin, self.device)
-            n_pos, rot_dim = cos_sin.shape
-            pos_ptr, axes = None, 1
+            rot = self._r
+            rot.cos_sin = cos_sin.data_ptr()
+            rot.n_positions, rot.rot_dim = cos_sin.shape
+            rot.interleaved = 1 if interleaved else 0
+            axes, rot.positions = 1, None
             if positions is not None:
                 axes = positions.shape[0] if positions.dim() == 2 else 1
-                _check_tensor("positions", positions, torch.int32, (axes, n) if positions.dim() == 2 else (n,), align=4)
-                _same_device("positions", positions, self.device)
-                pos_ptr = positions.data_ptr()
+                rot.positions = self._ints("positions", positions, (axes, n) if positions.dim() == 2 else (n,))
             if not 1 <= axes <= 4:
                 raise ValueError(f"positions on {axes} axes: 1 to 4 are supported")
             if sections is None:
                 if axes != 1:
                     raise ValueError("positions on several axes need sections")
-                sections = (rot_dim // 2,)
+                sections = (rot.rot_dim // 2,)
             if len(sections) != axes:
                 raise ValueError(f"{len(sections)} sections for positions on {axes} axes")
-            rot = Rotation(cos_sin.data_ptr(), n_pos, rot_dim, int(bool(interleaved)), pos_ptr, axes,
-                           (ctypes.c_int * 4)(*sections))
+            rot.n_axes = axes
+            rot.sections[:axes] = sections
             if q is not None:
                 qs = self._packed("q", q, self.n_q_heads)
                 if q.shape[0] != n:
                     raise ValueError(f"q has {q.shape[0]} tokens, k_new {n}")
                 if q_out is None:
-                    q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+                    q_out = self._empty_like(q, memory_format=self._contiguous)
                 else:
                     _check_tensor("q_out", q_out, self.dtype, q.shape)
                     _same_device("q_out", q_out, self.device)
                 q_ptr, out_ptr = q.data_ptr(), q_out.data_ptr()
-        self._launch("rq_paged_append", stream, self.handle, layer, ctypes.byref(batch),
-                     ctypes.byref(rot) if rot is not None else None, k_new.data_ptr(), ks, v_new.data_ptr(), vs,
-                     q_ptr, qs, out_ptr, self.append_status.data_ptr())
+        self._launch("rq_paged_append", self._append_fn, stream, self.handle, layer, self._b_ref, None if rot is None else self._r_ref,
+                     k_new.data_ptr(), ks, v_new.data_ptr(), vs, q_ptr, qs, out_ptr, self._status_ptr)
         return q_out
 
     def rq_paged_workspace_bytes(self, n_seqs, n_tokens) -> int:
@@ -462,7 +477,7 @@ class PagedKVCache:
 
         nb = self.rq_paged_workspace_bytes(n_seqs, n_tokens)
         ws = torch.empty(nb, dtype=torch.uint8, device=self.k_pages.device)
-        self._launch("rq_decode_workspace_init", stream, _dptr(ws), nb)
+        self._launch("rq_decode_workspace_init", lib().rq_decode_workspace_init, stream, _dptr(ws), nb)
         return ws
 
     def rq_paged_attention(self, layer, q, page_table, kv_lens, cu_new=None, max_new=None, window=0, n_sink=0,
@@ -475,7 +490,7 @@ class PagedKVCache:
         type; rows behind the last sequence are left as they were.  lse: fp32
         [tokens, n_q_heads], filled with the natural logarithm of each
         softmax's denominator."""
-        return self._attention("rq_paged_attention", (), layer, q, page_table, kv_lens, cu_new, max_new, window,
+        return self._attention("rq_paged_attention", self._attention_fns[0], (), layer, q, page_table, kv_lens, cu_new, max_new, window,
                                n_sink, softmax_scale, out, lse, workspace, stream)
 
     def rq_paged_shared_attention(self, layer, q, prefix_pages, prefix_len, page_table, kv_lens, cu_new=None,
@@ -485,40 +500,35 @@ class PagedKVCache:
         tokens in prefix_pages (int32 [ceil(prefix_len / page_size)]), which
         are read once for the whole batch; page_table and kv_lens count what
         follows the prefix, window and n_sink count from its first token."""
-        import torch
-
-        _check_tensor("prefix_pages", prefix_pages, torch.int32, align=4)
-        _same_device("prefix_pages", prefix_pages, self.device)
+        pages = self._ints("prefix_pages", prefix_pages, (prefix_pages.numel(),))
         prefix_len = int(prefix_len)
         if prefix_len < 0 or prefix_pages.numel() * self.page_size < prefix_len:
             raise ValueError(f"{prefix_pages.numel()} pages of {self.page_size} do not hold {prefix_len} tokens")
-        return self._attention("rq_paged_shared_attention", (prefix_pages.data_ptr(), prefix_len), layer, q,
+        return self._attention("rq_paged_shared_attention", self._attention_fns[1], (pages, prefix_len), layer, q,
                                page_table, kv_lens, cu_new, max_new, window, n_sink, softmax_scale, out, lse,
                                workspace, stream)
 
-    def _attention(self, func, prefix, layer, q, page_table, kv_lens, cu_new, max_new, window, n_sink, softmax_scale,
-                   out, lse, workspace, stream):
-        import torch
-
+    def _attention(self, func, fn, prefix, layer, q, page_table, kv_lens, cu_new, max_new, window, n_sink,
+                   softmax_scale, out, lse, workspace, stream):
         qs = self._packed("q", q, self.n_q_heads)
         n = q.shape[0]
-        batch = self._batch(n, page_table, kv_lens, cu_new, max_new)
+        n_seqs = self._batch(n, page_table, kv_lens, cu_new, max_new)
         if out is None:
-            out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+            out = self._empty_like(q, memory_format=self._contiguous)
         else:
             _check_tensor("out", out, self.dtype, q.shape)
             _same_device("out", out, self.device)
+        lse_ptr = None
         if lse is not None:
-            _check_tensor("lse", lse, torch.float32, (n, self.n_q_heads), align=4)
+            _check_tensor("lse", lse, self._f32, (n, self.n_q_heads), align=4)
             _same_device("lse", lse, self.device)
+            lse_ptr = lse.data_ptr()
         if workspace is None:
-            workspace = self.make_workspace(batch.n_seqs, n, stream)
-        else:
-            _check_tensor("workspace", workspace, torch.uint8)
-            _same_device("workspace", workspace, self.device)
-        self._launch(func, stream, self.handle, layer, ctypes.byref(batch), *prefix, q.data_ptr(), qs, out.data_ptr(),
-                     None if lse is None else lse.data_ptr(), float(softmax_scale), int(window), int(n_sink),
-                     workspace.data_ptr(), workspace.numel())
+            workspace = self.make_workspace(n_seqs, n, stream)
+        elif workspace.get_device() != self.device or not workspace.is_contiguous():
+            raise ValueError("workspace must be a contiguous tensor on the device of the pages")
+        self._launch(func, fn, stream, self.handle, layer, self._b_ref, *prefix, q.data_ptr(), qs, out.data_ptr(), lse_ptr,
+                     softmax_scale, window, n_sink, workspace.data_ptr(), workspace.nbytes)
         return out
 
     def read_status(self, workspace=None) -> int:

@@ -691,14 +691,16 @@ __global__ void __launch_bounds__(128) paged_merge_kernel(const __grid_constant_
   const int lane = threadIdx.x & 31;
   const int64_t row = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5);
   const int64_t n_rows = (int64_t)a.b.n_tokens * a.b.hq;
-  griddep_wait();
   griddep_launch_dependents();
-  if (row >= n_rows) return;
+  if (row >= n_rows) {
+    griddep_wait();
+    return;
+  }
   const int token = (int)(row / a.b.hq);
   const int b = seq_of(a.b, token);
-  if (b < 0) return;
-  const Seq s = load_seq(a.b, b);
-  if (token < s.t0 || token >= s.t0 + s.n) return;
+  const Seq s = b >= 0 ? load_seq(a.b, b) : Seq{0, 0, 0};
+  griddep_wait();
+  if (token < s.t0 || token >= s.t0 + s.n) return;  // no sequence's
   const bool few = a.few_rows_apart && (s.n << a.b.g_shift) <= kDecodeRows;
   if (few && shared == 0) return;  // the decode kernel wrote the result
   const int slots = shared + (few ? 1 : own);
@@ -713,7 +715,7 @@ __global__ void __launch_bounds__(128) paged_merge_kernel(const __grid_constant_
 #pragma unroll
   for (int e = 0; e < E; ++e) v[e] = 0.f;
   // (a part that saw nothing holds zeros and the maximum -inf: weight 0)
-#pragma unroll 8
+#pragma unroll 16
   for (int k = 0; k < slots; ++k) {
     const int64_t at = k * n_rows + row;
     const float2 x = __ldg(reinterpret_cast<const float2*>(a.rows_ml + 2 * at));
