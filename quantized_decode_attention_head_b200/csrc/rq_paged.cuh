@@ -25,8 +25,16 @@ __device__ __forceinline__ bool bar_wait(uint64_t* bar, uint32_t parity) {
   }
 }
 
+// The lowest n bits (n <= 0: none, n >= 32: all).
+__device__ __forceinline__ uint32_t low_bits(int n) { return n >= 32 ? 0xFFFFFFFFu : n <= 0 ? 0u : (1u << n) - 1u; }
+
 __device__ __forceinline__ void flag_index(int* status) {
   if (status) *status = kDeviceIndex;
+}
+
+// Brings a tensor map into the descriptor cache.
+__device__ __forceinline__ void prefetch_map(const CUtensorMap* map) {
+  asm volatile("prefetch.tensormap [%0];\n" ::"l"(map) : "memory");
 }
 
 // 16-bit element types of the pages: conversions to and from fp32.

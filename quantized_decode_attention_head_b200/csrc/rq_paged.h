@@ -40,6 +40,7 @@ struct PagedAppendArgs {
   const int* positions;
   int n_positions, rot, interleaved, n_axes;
   int sections[kMaxAxes];
+  int block_tokens;  // tokens of a block (set by the launch)
 };
 
 struct PagedAttnArgs {

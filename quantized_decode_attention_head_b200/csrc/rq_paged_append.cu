@@ -2,18 +2,29 @@
 // position, keys and values written to their pages, in one pass.
 //
 // Every element is read once and written once; there is no reuse but that of
-// a position's cosines and sines by the heads of its token, which L1 serves.
-// Memory bound: (2 Hq + 4 Hkv) D 16-bit values a token.  A work item is one
-// 16-byte vector of a head, or the two vectors whose channels are paired; a
-// block takes one token, its items one after another, so that neighbouring
-// threads move neighbouring vectors.
+// a position's cosines and sines by the heads of its token.  Memory bound:
+// (2 Hq + 4 Hkv) D 16-bit values a token.  A lane owns one 16-byte vector of
+// a head, or the two vectors whose channels are paired, with their cosines and
+// sines in registers, and walks over the heads of its token, several loads in
+// flight; neighbouring lanes own neighbouring vectors.  A block takes several
+// tokens, whose places (sequence, page, positions: a chain of dependent
+// loads) are found side by side; one token a block when there are few, where
+// the call is that chain's latency.
 #include "rq_paged.cuh"
 #include "rq_paged_launch.h"
 
 namespace rq {
 namespace {
 
-constexpr int kThreads = 128;
+constexpr int kThreads = 256;
+constexpr int kMaxTokens = 8;  // of a block
+
+// Where a token goes.
+struct Place {
+  int64_t row;         // its row of kv head 0 in the pages, -1: not written
+  int pos[kMaxAxes];   // its position on each axis
+  int state;           // 0: no sequence's, 1: whole, 2: position outside the table of angles
+};
 
 // (a, b) turned by (c, s): products and differences each rounded once in fp32
 // (no contraction), so that the result does not depend on the compiler.
@@ -33,119 +44,173 @@ __device__ __forceinline__ int pair_position(const PagedAppendArgs& a, const int
   return pos[ax];
 }
 
-template <class T, int D>
-__global__ void __launch_bounds__(kThreads) paged_append_kernel(const __grid_constant__ PagedAppendArgs a) {
-  griddep_wait();
-  griddep_launch_dependents();
-  const int t = blockIdx.x;
-  const int seq = seq_of(a.b, t);
-  if (seq < 0) return;
-  const Seq s = load_seq(a.b, seq);
-  if (t < s.t0 || t >= s.t0 + s.n) return;  // offsets out of order: the token has no sequence
-  const int place = s.len - s.n + (t - s.t0);
-  int64_t row = -1;
-  if (place >= 0) {
-    row = page_row(a.b, __ldg(a.b.table + (int64_t)seq * a.b.width + (place >> a.b.page_shift)));
-    if (row >= 0) row += place & ((1 << a.b.page_shift) - 1);
+// Cosines and sines of N pairs from j on: wide loads when one position serves
+// them all (an axis may end between two of them).
+template <int N>
+__device__ __forceinline__ void load_angles(const PagedAppendArgs& a, const int* pos, int j, float (&c)[8], float (&s)[8]) {
+  const int half = a.rot / 2, p0 = pair_position(a, pos, j);
+  bool one = true;
+  if (a.n_axes > 1) {
+#pragma unroll
+    for (int e = 1; e < N; ++e) one &= pair_position(a, pos, j + e) == p0;
+  }
+  if (one) {
+    const float4* tc = reinterpret_cast<const float4*>(a.cos_sin + (int64_t)p0 * a.rot + j);
+    const float4* ts = reinterpret_cast<const float4*>(a.cos_sin + (int64_t)p0 * a.rot + half + j);
+#pragma unroll
+    for (int e = 0; e < N / 4; ++e) {
+      const float4 x = __ldg(tc + e), y = __ldg(ts + e);
+      c[4 * e] = x.x, c[4 * e + 1] = x.y, c[4 * e + 2] = x.z, c[4 * e + 3] = x.w;
+      s[4 * e] = y.x, s[4 * e + 1] = y.y, s[4 * e + 2] = y.z, s[4 * e + 3] = y.w;
+    }
   } else {
-    flag_index(a.b.status);
-  }
-  // the token's position on each axis; outside the table of angles: bad
-  int pos[kMaxAxes];
-  bool bad = false;
-  if (a.cos_sin) {
 #pragma unroll
-    for (int k = 0; k < kMaxAxes; ++k) {
-      pos[k] = 0;
-      if (k < a.n_axes) {
-        pos[k] = a.positions ? __ldg(a.positions + (int64_t)k * a.b.n_tokens + t) : place;
-        if ((unsigned)pos[k] >= (unsigned)a.n_positions) bad = true;
-      }
-    }
-    if (bad) flag_index(a.b.status);
-  }
-  const int rot = a.cos_sin ? a.rot : 0;
-  const int half = rot / 2;
-  // items of a head: half/8 pairs of vectors and the rest single vectors, or
-  // D/8 single vectors when the pairs are neighbours
-  const int pairs = a.interleaved ? 0 : half / 8;
-  const int per_head = D / 8 - pairs;
-  const int heads_q = a.q ? a.b.hq : 0;
-  const int items = (heads_q + 2 * a.b.hkv) * per_head;
-  const int item0 = blockIdx.y * kThreads + threadIdx.x;
-  for (int it = item0; it < items; it += gridDim.y * kThreads) {
-    const int h = it / per_head, v = it - h * per_head;
-    const uint16_t* src;
-    uint16_t* dst;
-    bool turns = true;
-    if (h < heads_q) {
-      src = a.q + t * a.q_stride + h * D;
-      dst = a.q_out + ((int64_t)t * a.b.hq + h) * D;
-    } else {
-      if (row < 0 || bad) continue;
-      const int kh = h - heads_q;
-      const bool key = kh < a.b.hkv;
-      const int hh = key ? kh : kh - a.b.hkv;
-      src = (key ? a.k_new + t * a.k_stride : a.v_new + t * a.v_stride) + hh * D;
-      dst = (key ? a.k_pages : a.v_pages) + (row + ((int64_t)hh << a.b.page_shift)) * D;
-      turns = key;
-    }
-    if (v < pairs) {
-      uint4 x = __ldg(reinterpret_cast<const uint4*>(src) + v);
-      uint4 y = __ldg(reinterpret_cast<const uint4*>(src + half) + v);
-      if (turns) {
-        uint32_t* xp = reinterpret_cast<uint32_t*>(&x);
-        uint32_t* yp = reinterpret_cast<uint32_t*>(&y);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int j = 8 * v + 2 * e;
-          const float2 lo = T::unpack(xp[e]), hi = T::unpack(yp[e]);
-          float2 r0 = make_float2(0.f, 0.f), r1 = r0;
-          if (!bad) {
-            const float* t0 = a.cos_sin + (int64_t)pair_position(a, pos, j) * rot;
-            const float* t1 = a.cos_sin + (int64_t)pair_position(a, pos, j + 1) * rot;
-            r0 = turn(lo.x, hi.x, __ldg(t0 + j), __ldg(t0 + half + j));
-            r1 = turn(lo.y, hi.y, __ldg(t1 + j + 1), __ldg(t1 + half + j + 1));
-          }
-          xp[e] = T::pack(r0.x, r1.x);
-          yp[e] = T::pack(r0.y, r1.y);
-        }
-      }
-      reinterpret_cast<uint4*>(dst)[v] = x;
-      reinterpret_cast<uint4*>(dst + half)[v] = y;
-    } else {
-      const int vv = a.interleaved ? v : v + pairs;
-      uint4 x = __ldg(reinterpret_cast<const uint4*>(src) + vv);
-      if (turns && (bad || 8 * vv < rot)) {
-        uint32_t* xp = reinterpret_cast<uint32_t*>(&x);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int j = 4 * vv + e;
-          const float2 ab = T::unpack(xp[e]);
-          float2 r = make_float2(0.f, 0.f);
-          if (!bad) {
-            const float* tj = a.cos_sin + (int64_t)pair_position(a, pos, j) * rot;
-            r = turn(ab.x, ab.y, __ldg(tj + j), __ldg(tj + half + j));
-          }
-          xp[e] = T::pack(r.x, r.y);
-        }
-      }
-      reinterpret_cast<uint4*>(dst)[vv] = x;
+    for (int e = 0; e < N; ++e) {
+      const float* t = a.cos_sin + (int64_t)pair_position(a, pos, j + e) * a.rot;
+      c[e] = __ldg(t + j + e);
+      s[e] = __ldg(t + half + j + e);
     }
   }
 }
 
-template <class T>
-cudaError_t launch(const PagedAppendArgs& a, int head_dim, cudaStream_t s) {
-  const dim3 grid(a.b.n_tokens, 1);
-  return head_dim == 128 ? launch_pdl<paged_append_kernel<T, 128>>(grid, kThreads, 0, s, a)
-                         : launch_pdl<paged_append_kernel<T, 64>>(grid, kThreads, 0, s, a);
+__device__ __forceinline__ Place place_of(const PagedAppendArgs& a, int t) {
+  Place o = {-1, {0, 0, 0, 0}, 0};
+  if (t >= a.b.n_tokens) return o;
+  const int seq = seq_of(a.b, t);
+  if (seq < 0) return o;
+  const Seq s = load_seq(a.b, seq);
+  if (t < s.t0 || t >= s.t0 + s.n) return o;  // offsets out of order: the token has no sequence
+  const int at = s.len - s.n + (t - s.t0);
+  o.state = 1;
+  if (a.cos_sin) {
+#pragma unroll
+    for (int k = 0; k < kMaxAxes; ++k)
+      if (k < a.n_axes) {
+        o.pos[k] = a.positions ? __ldg(a.positions + (int64_t)k * a.b.n_tokens + t) : at;
+        if ((unsigned)o.pos[k] >= (unsigned)a.n_positions) o.state = 2;
+      }
+  }
+  if (at >= 0) {
+    o.row = page_row(a.b, __ldg(a.b.table + (int64_t)seq * a.b.width + (at >> a.b.page_shift)));
+    if (o.row >= 0) o.row += at & ((1 << a.b.page_shift) - 1);
+  }
+  if (at < 0 || o.state == 2) flag_index(a.b.status);
+  if (o.state == 2) o.row = -1;
+  return o;
+}
+
+// kPairs: channels j and j + rot/2 are paired (else 2j and 2j + 1).
+template <class T, int D, bool kPairs>
+__global__ void __launch_bounds__(kThreads) paged_append_kernel(const __grid_constant__ PagedAppendArgs a) {
+  griddep_wait();
+  griddep_launch_dependents();
+  __shared__ Place places[kMaxTokens];
+  const int tokens = a.block_tokens;
+  if (threadIdx.x < tokens) places[threadIdx.x] = place_of(a, blockIdx.x * tokens + threadIdx.x);
+  __syncthreads();
+  const int rot = a.cos_sin ? a.rot : 0, half = rot / 2;
+  // a head's items: half/8 pairs of vectors and the rest single vectors, or
+  // D/8 single vectors when neighbouring channels are paired
+  const int pairs = kPairs ? half / 8 : 0;
+  const int per_head = D / 8 - pairs;
+  const int lanes = tokens * per_head, groups = kThreads / lanes;  // lanes of a group walk over the same heads
+  const int group = threadIdx.x / lanes, x = threadIdx.x - group * lanes;
+  const int token = x / per_head, v = x - token * per_head;
+  if (group >= groups) return;
+  const Place& p = places[token];
+  if (p.state == 0) return;
+  const int64_t t = (int64_t)blockIdx.x * tokens + token;
+  const bool paired = v < pairs;
+  const int first = kPairs && !paired ? v + pairs : v;  // the item's (first) vector of a head
+  const bool turns = paired || (!kPairs && 8 * v < rot);
+  float c[8], s[8];
+  if (turns && p.state == 1) {
+    if (paired)
+      load_angles<8>(a, p.pos, 8 * v, c, s);
+    else
+      load_angles<4>(a, p.pos, 4 * v, c, s);
+  }
+  const int heads_q = a.q ? a.b.hq : 0, heads = heads_q + 2 * a.b.hkv;
+  const int64_t row = p.row;
+  auto source = [&](int h) {
+    if (h < heads_q) return a.q + t * a.q_stride + h * D;
+    h -= heads_q;
+    return h < a.b.hkv ? a.k_new + t * a.k_stride + h * D : a.v_new + t * a.v_stride + (h - a.b.hkv) * D;
+  };
+  constexpr int kAhead = 4;  // heads loaded at once
+  for (int h0 = group; h0 < heads; h0 += kAhead * groups) {
+    uint4 lo[kAhead], hi[kAhead];
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+      const int h = h0 + i * groups;
+      if (h < heads) {
+        const uint16_t* src = source(h);
+        lo[i] = __ldg(reinterpret_cast<const uint4*>(src) + first);
+        if (paired) hi[i] = __ldg(reinterpret_cast<const uint4*>(src + half) + first);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+      const int h = h0 + i * groups;
+      if (h >= heads) break;
+      uint16_t* dst;
+      bool turn_it = turns;
+      if (h < heads_q) {
+        dst = a.q_out + (t * a.b.hq + h) * D;
+        if (p.state == 2) {  // no such position
+          lo[i] = hi[i] = make_uint4(0, 0, 0, 0);
+          turn_it = false;
+        }
+      } else {
+        if (row < 0) break;
+        const int kh = h - heads_q;
+        const bool key = kh < a.b.hkv;
+        const int64_t hh = key ? kh : kh - a.b.hkv;
+        dst = (key ? a.k_pages : a.v_pages) + (row + (hh << a.b.page_shift)) * D;
+        turn_it = turns && key;
+      }
+      if (turn_it) {
+        uint32_t* xp = reinterpret_cast<uint32_t*>(&lo[i]);
+        if (paired) {
+          uint32_t* yp = reinterpret_cast<uint32_t*>(&hi[i]);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float2 x2 = T::unpack(xp[e]), y2 = T::unpack(yp[e]);
+            const float2 r0 = turn(x2.x, y2.x, c[2 * e], s[2 * e]), r1 = turn(x2.y, y2.y, c[2 * e + 1], s[2 * e + 1]);
+            xp[e] = T::pack(r0.x, r1.x);
+            yp[e] = T::pack(r0.y, r1.y);
+          }
+        } else {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float2 x2 = T::unpack(xp[e]);
+            const float2 r = turn(x2.x, x2.y, c[e], s[e]);
+            xp[e] = T::pack(r.x, r.y);
+          }
+        }
+      }
+      reinterpret_cast<uint4*>(dst)[first] = lo[i];
+      if (paired) reinterpret_cast<uint4*>(dst + half)[first] = hi[i];
+    }
+  }
+}
+
+template <class T, int D>
+cudaError_t launch(PagedAppendArgs a, cudaStream_t s) {
+  // tokens of a block: 8 when that still leaves four blocks an SM
+  static_assert(kMaxTokens * D / 8 <= kThreads, "one lane an item at least");
+  a.block_tokens = 1;
+  while (a.block_tokens < kMaxTokens && a.b.n_tokens / (2 * a.block_tokens) >= 4 * 148) a.block_tokens *= 2;
+  const dim3 grid((unsigned)((a.b.n_tokens + a.block_tokens - 1) / a.block_tokens));
+  return a.interleaved ? launch_pdl<paged_append_kernel<T, D, false>>(grid, kThreads, 0, s, a)
+                       : launch_pdl<paged_append_kernel<T, D, true>>(grid, kThreads, 0, s, a);
 }
 
 }  // namespace
 
 cudaError_t launch_paged_append(const PagedAppendArgs& a, int head_dim, int dtype, cudaStream_t s) {
-  return dtype == 0 ? launch<Bf16>(a, head_dim, s) : launch<Fp16>(a, head_dim, s);
+  if (head_dim == 128) return dtype == 0 ? launch<Bf16, 128>(a, s) : launch<Fp16, 128>(a, s);
+  return dtype == 0 ? launch<Bf16, 64>(a, s) : launch<Fp16, 64>(a, s);
 }
 
 }  // namespace rq

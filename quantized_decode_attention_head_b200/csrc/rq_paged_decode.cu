@@ -52,7 +52,8 @@ struct Walk {
   int lo, sink;        // tokens [0, sink) and [lo, len) are seen by some query
   int ns, lo_c, chunks, units;
 };
-__device__ __forceinline__ Walk walk_of(const PagedAttnArgs& a, int b) {
+// (not inlined: the kernel's start is bound by fetching its code)
+__device__ __noinline__ Walk walk_of(const PagedAttnArgs& a, int b) {
   Walk w = {};
   if (b >= a.b.n_seqs) return w;  // no units
   const Seq s = load_seq(a.b, b);
@@ -128,6 +129,10 @@ __global__ void __launch_bounds__(NW * 32, 1)
   mbar_fence_init();
   // the first kernel of a call, or after another of the same call: nothing
   // that one writes is read here
+  if (threadIdx.x == 0) {
+    prefetch_map(&kmap);
+    prefetch_map(&vmap);
+  }
   if (a.first) griddep_wait();
   griddep_launch_dependents();
 
@@ -341,13 +346,16 @@ __global__ void __launch_bounds__(NW * 32, 1)
                          (a.window == 0 || t > p_first + w.n - 1 - a.window || t + kChunk <= w.sink);
       if (!whole) {
 #pragma unroll
-        for (int nb = 0; nb < 4; ++nb)
+        for (int rr = 0; rr < 2; ++rr) {
+          // keys of the chunk that the row sees: up to itself, and in its window or among the first
+          const int w_lo = a.window > 0 ? p_row[rr] + 1 - a.window : 0;
+          const uint32_t see = (lives & low_bits(p_row[rr] + 1 - t) & (~low_bits(w_lo - t) | low_bits(w.sink - t))) >> (2 * tig);
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const int col = nb * 8 + 2 * tig + (e & 1), jj = t + col, p = p_row[e >> 1];
-            const bool see = ((lives >> col) & 1u) && jj <= p && (a.window == 0 || p - jj < a.window || jj < w.sink);
-            if (!see) s[nb][e] = -INFINITY;
-          }
+          for (int nb = 0; nb < 4; ++nb)
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+              if (!((see >> (8 * nb + e)) & 1u)) s[nb][2 * rr + e] = -INFINITY;
+        }
       }
 #pragma unroll
       for (int rr = 0; rr < 2; ++rr) {

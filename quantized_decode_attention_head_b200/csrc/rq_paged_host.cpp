@@ -122,9 +122,8 @@ rq_status prepare(rq_paged_cache* c) {
 
 // CTAs among which the prompt kernel divides the keys of the same rows: as
 // many as fill the device once, while each keeps at least four tiles of 128 keys.
-int splits_of(const rq_paged_cache* c, int64_t blocks, int64_t keys, int window, int n_sink, int max_new) {
+int splits_of(const rq_paged_cache* c, int64_t blocks, int64_t keys, int window, int n_sink, int max_new, int sms) {
   const int64_t ctas = blocks * c->cfg.n_kv_heads;
-  const int64_t sms = decode_ctas(c);
   if (ctas <= 0) return 1;
   const int64_t reach = (int64_t)window + n_sink + max_new;
   if (window > 0 && reach < keys) keys = reach;
@@ -194,10 +193,36 @@ rq_status attention(rq_paged_cache* c, int layer, const rq_paged_batch* batch, c
   if (prompt) {
     const int64_t seqs = decode ? all_rows / (rq::kDecodeRows + 1) : all_rows;  // that can have a block of their own
     blocks = all_rows / rq::kPromptRows + (seqs < batch->n_seqs ? seqs : batch->n_seqs);
-    own = splits_of(c, blocks, (int64_t)batch->table_width * c->cfg.page_size, window, n_sink, batch->max_new);
+    own = splits_of(c, blocks, (int64_t)batch->table_width * c->cfg.page_size, window, n_sink, batch->max_new,
+                    decode_ctas(c));
   }
   const int64_t shared_blocks = (all_rows + rq::kPromptRows - 1) / rq::kPromptRows;
-  if (prefix_len > 0) shared = splits_of(c, shared_blocks, prefix_len, 0, 0, 0);
+  const bool side_by_side = prefix_len > 0 && decode && !prompt;
+  if (prefix_len > 0) {
+    int sms = decode_ctas(c);
+    if (side_by_side) {
+      // The decode kernel (what follows the prefix) and the prompt kernel (the
+      // prefix) run side by side, on SMs of their own: a unit of either, 128
+      // keys of one sequence or of 256 rows, takes about as long (1.9 us
+      // measured), so the SMs are divided by the units.  Lengths are on the
+      // device; what is known here is the width of the table, of which
+      // sequences of different lengths fill about half.
+      const int64_t tail = (int64_t)batch->n_seqs * (((int64_t)batch->table_width * c->cfg.page_size + 255) / 256);
+      const int64_t front = shared_blocks * (((int64_t)prefix_len + 127) / 128);
+      int64_t x = sms * tail / (tail + front);
+      if (x < 1) x = 1;
+      if (x > sms - c->cfg.n_kv_heads) x = sms - c->cfg.n_kv_heads;  // one CTA a head for the prefix
+      if (x < 1) x = 1;
+      a.n_ctas = (int)x;
+      sms -= (int)x;
+    }
+    shared = splits_of(c, shared_blocks, prefix_len, 0, 0, 0, sms);
+    if (side_by_side) {
+      // what the splits leave over
+      const int64_t left = decode_ctas(c) - shared_blocks * c->cfg.n_kv_heads * shared;
+      if (left > a.n_ctas) a.n_ctas = (int)left;
+    }
+  }
   if (blocks > 0x7FFFFFFF || shared_blocks > 0x7FFFFFFF) return RQ_ERR_UNSUPPORTED;
   const bool merge = shared > 0 || own > 1;
   if (merge) {
@@ -206,7 +231,15 @@ rq_status attention(rq_paged_cache* c, int layer, const rq_paged_batch* batch, c
   }
   cudaError_t e = cudaSuccess;
   a.first = 1;
-  if (shared > 0) {
+  auto run_decode = [&]() {
+    rq::PagedAttnArgs f = a;
+    f.row_slot = shared;
+    if (shared == 0) f.rows_o = f.rows_ml = nullptr;  // straight to out
+    e = rq::launch_paged_decode(c->k32, c->v32, f, d, type, stream);
+    a.first = 0;
+  };
+  if (side_by_side) run_decode();
+  if (e == cudaSuccess && shared > 0) {
     a.over_prefix = 1;
     e = rq::launch_paged_prompt(c->kp, c->vp, a, (int)shared_blocks, shared, d, type, stream);
     a.over_prefix = a.first = 0;
@@ -216,11 +249,7 @@ rq_status attention(rq_paged_cache* c, int layer, const rq_paged_batch* batch, c
     e = rq::launch_paged_prompt(c->kp, c->vp, a, (int)blocks, own, d, type, stream);
     a.first = 0;
   }
-  if (e == cudaSuccess && decode) {
-    rq::PagedAttnArgs f = a;
-    if (shared == 0) f.rows_o = f.rows_ml = nullptr;  // straight to out
-    e = rq::launch_paged_decode(c->k32, c->v32, f, d, type, stream);
-  }
+  if (e == cudaSuccess && decode && !side_by_side) run_decode();
   if (e == cudaSuccess && merge) e = rq::launch_paged_merge(a, shared, own, d, type, stream);
   return cuda_status(e);
 }

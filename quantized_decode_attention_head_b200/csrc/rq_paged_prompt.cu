@@ -144,9 +144,6 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   return d;
 }
 
-// The lowest n bits (n <= 0: none, n >= 32: all).
-__device__ __forceinline__ uint32_t low_bits(int n) { return n >= 32 ? 0xFFFFFFFFu : n <= 0 ? 0u : (1u << n) - 1u; }
-
 // A warp's wait: all lanes go on, or none (the tcgen05 accesses need the whole warp).
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity) {
   return __all_sync(0xffffffffu, bar_wait(bar, parity));
@@ -202,6 +199,10 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   // the first kernel of a call, or after another of the same call: nothing
   // that one writes is read here before it ends
+  if (threadIdx.x == 0) {
+    prefetch_map(&kmap);
+    prefetch_map(&vmap);
+  }
   if (a.first) griddep_wait();
   griddep_launch_dependents();
 
