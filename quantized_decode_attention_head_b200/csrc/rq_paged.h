@@ -60,16 +60,16 @@ struct PagedAttnArgs {
   int over_prefix;        // prompt kernel: all rows of the batch over the prefix
   int few_rows_apart;     // sequences of at most kDecodeRows rows are the decode kernel's
   int few_rows_only;      // the call said that no sequence has more than 16 rows a kv head
-  int n_ctas;             // CTAs of the decode kernel, at most kMaxParts
-  float* parts;           // its partial states: two slots of part_floats(D) a CTA
-  uint32_t* counters;     // one a CTA: parts of the stream that begins to be split there
+  int n_ctas;             // CTAs of the decode kernel, two teams each
+  float* parts;           // its partial states: two slots of part_floats(D) a team
+  uint32_t* counters;     // one a team: parts of the stream that begins to be split there
   float* rows_o;          // null: results go to out; else partial states of whole rows,
   float* rows_ml;         //   [row_slot][n_tokens][hq][D] and [..][2] (maximum in log2 units, sum)
   int row_slot;
 };
 
-// Most CTAs among which one stream of the decode kernel can be split.
-constexpr int kMaxParts = 160;
+constexpr int kMaxCtas = 160;             // of the decode kernel
+constexpr int kMaxParts = 2 * kMaxCtas;  // teams among which it divides its work
 constexpr int kPromptRows = 256;  // rows of a CTA of the prompt kernel
 constexpr int kMaxSplits = 128;   // CTAs among which it splits the keys of the same rows
 constexpr int kDecodeRows = 16;  // rows of a kv head that the decode kernel takes

@@ -15,7 +15,7 @@ struct rq_paged_cache {
   uint16_t *k, *v;
   int sms;
   bool mapped;
-  CUtensorMap k32, v32;  // boxes of the decode kernel: 64 channels of 32 tokens (or of a page, if shorter)
+  CUtensorMap k16, v16;  // boxes of the decode kernel: all channels of 16 tokens
   CUtensorMap kp, vp;    // boxes of the prompt kernel: 64 channels of a page
 };
 
@@ -73,27 +73,27 @@ size_t parts_bytes(const rq_paged_cache* c) {
 // splits keep CTAs (256 rows a kv head each) at or below one a SM.
 int64_t part_rows(const rq_paged_cache* c, int n_tokens) {
   const int64_t rows = (int64_t)n_tokens * c->cfg.n_q_heads;
-  const int64_t most = (int64_t)rq::kMaxParts * rq::kPromptRows;
+  const int64_t most = (int64_t)rq::kMaxCtas * rq::kPromptRows;
   const int64_t split = rows * rq::kMaxSplits < most ? rows * rq::kMaxSplits : most;
   return rows > split ? rows : split;
 }
 
-int decode_ctas(const rq_paged_cache* c) { return c->sms < rq::kMaxParts ? c->sms : rq::kMaxParts; }
+int decode_ctas(const rq_paged_cache* c) { return c->sms < rq::kMaxCtas ? c->sms : rq::kMaxCtas; }
 
 typedef CUresult (*EncodeTiled)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
                                 const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
                                 CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
 
-// The pages as a matrix [rows][head_dim], read in boxes of 64 channels (128
-// bytes, swizzled) and `rows` rows.
-bool encode(EncodeTiled fn, const rq_paged_cache* c, void* base, int box_rows, CUtensorMap* map) {
+// The pages as [head_dim / 64][rows][64 channels], read in boxes of `panels`
+// panels of `rows` rows of 64 channels (128 bytes, swizzled).
+bool encode(EncodeTiled fn, const rq_paged_cache* c, void* base, int box_rows, int panels, CUtensorMap* map) {
   const rq_paged_config& f = c->cfg;
-  const cuuint64_t dims[2] = {(cuuint64_t)f.head_dim,
-                              (cuuint64_t)f.n_layers * f.n_pages * f.n_kv_heads * f.page_size};
-  const cuuint64_t strides[1] = {(cuuint64_t)f.head_dim * 2};
-  const cuuint32_t box[2] = {64, (cuuint32_t)box_rows};
-  const cuuint32_t elem[2] = {1, 1};
-  return fn(map, f.dtype == 0 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, base, dims,
+  const cuuint64_t dims[3] = {64, (cuuint64_t)f.n_layers * f.n_pages * f.n_kv_heads * f.page_size,
+                              (cuuint64_t)f.head_dim / 64};
+  const cuuint64_t strides[2] = {(cuuint64_t)f.head_dim * 2, 128};
+  const cuuint32_t box[3] = {64, (cuuint32_t)box_rows, (cuuint32_t)panels};
+  const cuuint32_t elem[3] = {1, 1, 1};
+  return fn(map, f.dtype == 0 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, base, dims,
             strides, box, elem, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
@@ -111,10 +111,9 @@ rq_status prepare(rq_paged_cache* c) {
   if (d == cudaSuccess) d = cudaDeviceGetAttribute(&c->sms, cudaDevAttrMultiProcessorCount, dev);
   if (d != cudaSuccess) return cuda_status(d);
   const EncodeTiled enc = reinterpret_cast<EncodeTiled>(fn);
-  const int box = c->cfg.page_size < 32 ? c->cfg.page_size : 32;
-  const int page = c->cfg.page_size;
-  if (!encode(enc, c, c->k, box, &c->k32) || !encode(enc, c, c->v, box, &c->v32) ||
-      !encode(enc, c, c->k, page, &c->kp) || !encode(enc, c, c->v, page, &c->vp))
+  const int page = c->cfg.page_size, panels = c->cfg.head_dim / 64;
+  if (!encode(enc, c, c->k, 16, panels, &c->k16) || !encode(enc, c, c->v, 16, panels, &c->v16) ||
+      !encode(enc, c, c->k, page, 1, &c->kp) || !encode(enc, c, c->v, page, 1, &c->vp))
     return cuda_status(cudaErrorInvalidValue);
   c->mapped = true;
   return RQ_OK;
@@ -235,7 +234,7 @@ rq_status attention(rq_paged_cache* c, int layer, const rq_paged_batch* batch, c
     rq::PagedAttnArgs f = a;
     f.row_slot = shared;
     if (shared == 0) f.rows_o = f.rows_ml = nullptr;  // straight to out
-    e = rq::launch_paged_decode(c->k32, c->v32, f, d, type, stream);
+    e = rq::launch_paged_decode(c->k16, c->v16, f, d, type, stream);
     a.first = 0;
   };
   if (side_by_side) run_decode();

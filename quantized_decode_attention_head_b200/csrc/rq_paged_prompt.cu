@@ -130,11 +130,12 @@ __host__ __device__ constexpr uint32_t instr_desc(int type, bool b_mn, int m, in
          (uint32_t)(m >> 4) << 24;
 }
 
-__device__ __forceinline__ void tma_box(uint32_t dst, const CUtensorMap* map, int x, int y, uint64_t* bar) {
+// A page's rows from row y on, 64 channels (panel p).
+__device__ __forceinline__ void tma_box(uint32_t dst, const CUtensorMap* map, int p, int y, uint64_t* bar) {
   asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];\n" ::"r"(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];\n" ::"r"(
           dst),
-      "l"(map), "r"(x), "r"(y), "r"(smem_u32(bar))
+      "l"(map), "r"(0), "r"(y), "r"(p), "r"(smem_u32(bar))
       : "memory");
 }
 
@@ -387,7 +388,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               if (row[g] >= 0) {
 #pragma unroll
                 for (int p = 0; p < C::P; ++p)
-                  tma_box(dst + p * C::PANEL + (g << a.b.page_shift) * 128, kv ? &vmap : &kmap, 64 * p, row[g], full);
+                  tma_box(dst + p * C::PANEL + (g << a.b.page_shift) * 128, kv ? &vmap : &kmap, p, row[g], full);
               }
           }
         }
