@@ -7,17 +7,18 @@
 // a head, or the two vectors whose channels are paired, with their cosines and
 // sines in registers, and walks over the heads of its token, several loads in
 // flight; neighbouring lanes own neighbouring vectors.  A block takes several
-// tokens, whose places (sequence, page, positions: a chain of dependent
-// loads) are found side by side; one token a block when there are few, where
-// the call is that chain's latency.
+// tokens at a time, and a warp of its own finds the places of the next ones
+// (sequence, page, positions: a chain of dependent loads) meanwhile; one token
+// a block when there are few, where the call is that chain's latency.
 #include "rq_paged.cuh"
 #include "rq_paged_launch.h"
 
 namespace rq {
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kMaxTokens = 8;  // of a block
+constexpr int kThreads = 256;  // that move data; one more warp finds the next tokens' places
+constexpr int kResident = 3;   // blocks an SM: 4 would spill registers (62 us for 50, 20k tokens of three axes)
+constexpr int kMaxTokens = 8;  // of a block at a time
 
 // Where a token goes.
 struct Place {
@@ -73,9 +74,10 @@ __device__ __forceinline__ void load_angles(const PagedAppendArgs& a, const int*
   }
 }
 
-__device__ __forceinline__ Place place_of(const PagedAppendArgs& a, int t) {
+__device__ __forceinline__ Place place_of(const PagedAppendArgs& a, int64_t t64) {
   Place o = {-1, {0, 0, 0, 0}, 0};
-  if (t >= a.b.n_tokens) return o;
+  if (t64 >= a.b.n_tokens) return o;
+  const int t = (int)t64;
   const int seq = seq_of(a.b, t);
   if (seq < 0) return o;
   const Seq s = load_seq(a.b, seq);
@@ -101,13 +103,30 @@ __device__ __forceinline__ Place place_of(const PagedAppendArgs& a, int t) {
 
 // kPairs: channels j and j + rot/2 are paired (else 2j and 2j + 1).
 template <class T, int D, bool kPairs>
-__global__ void __launch_bounds__(kThreads) paged_append_kernel(const __grid_constant__ PagedAppendArgs a) {
+__device__ __forceinline__ void move_tokens(const PagedAppendArgs& a, const Place* places, int64_t t0);
+
+// kPairs: channels j and j + rot/2 are paired (else 2j and 2j + 1).
+template <class T, int D, bool kPairs>
+__global__ void __launch_bounds__(kThreads + 32, kResident) paged_append_kernel(const __grid_constant__ PagedAppendArgs a) {
   griddep_wait();
   griddep_launch_dependents();
-  __shared__ Place places[kMaxTokens];
+  __shared__ Place places[2][kMaxTokens];
+  const int tokens = a.block_tokens, stride = gridDim.x * tokens;
+  const int finder = (int)threadIdx.x - kThreads;  // lane of the warp that finds places
+  int64_t t0 = (int64_t)blockIdx.x * tokens;
+  if (finder >= 0 && finder < tokens) places[0][finder] = place_of(a, t0 + finder);
+  for (int turn = 0; t0 < a.b.n_tokens; t0 += stride, turn ^= 1) {
+    __syncthreads();
+    if (finder < 0)
+      move_tokens<T, D, kPairs>(a, places[turn], t0);
+    else if (finder < tokens)
+      places[turn ^ 1][finder] = place_of(a, t0 + stride + finder);
+  }
+}
+
+template <class T, int D, bool kPairs>
+__device__ __forceinline__ void move_tokens(const PagedAppendArgs& a, const Place* places, int64_t t0) {
   const int tokens = a.block_tokens;
-  if (threadIdx.x < tokens) places[threadIdx.x] = place_of(a, blockIdx.x * tokens + threadIdx.x);
-  __syncthreads();
   const int rot = a.cos_sin ? a.rot : 0, half = rot / 2;
   // a head's items: half/8 pairs of vectors and the rest single vectors, or
   // D/8 single vectors when neighbouring channels are paired
@@ -119,7 +138,7 @@ __global__ void __launch_bounds__(kThreads) paged_append_kernel(const __grid_con
   if (group >= groups) return;
   const Place& p = places[token];
   if (p.state == 0) return;
-  const int64_t t = (int64_t)blockIdx.x * tokens + token;
+  const int64_t t = t0 + token;
   const bool paired = v < pairs;
   const int first = kPairs && !paired ? v + pairs : v;  // the item's (first) vector of a head
   const bool turns = paired || (!kPairs && 8 * v < rot);
@@ -137,7 +156,7 @@ __global__ void __launch_bounds__(kThreads) paged_append_kernel(const __grid_con
     h -= heads_q;
     return h < a.b.hkv ? a.k_new + t * a.k_stride + h * D : a.v_new + t * a.v_stride + (h - a.b.hkv) * D;
   };
-  constexpr int kAhead = 4;  // heads loaded at once
+  constexpr int kAhead = 2;  // heads loaded at once (4: fewer blocks an SM, 58 us for 50)
   for (int h0 = group; h0 < heads; h0 += kAhead * groups) {
     uint4 lo[kAhead], hi[kAhead];
 #pragma unroll
@@ -201,9 +220,11 @@ cudaError_t launch(PagedAppendArgs a, cudaStream_t s) {
   static_assert(kMaxTokens * D / 8 <= kThreads, "one lane an item at least");
   a.block_tokens = 1;
   while (a.block_tokens < kMaxTokens && a.b.n_tokens / (2 * a.block_tokens) >= 4 * 148) a.block_tokens *= 2;
-  const dim3 grid((unsigned)((a.b.n_tokens + a.block_tokens - 1) / a.block_tokens));
-  return a.interleaved ? launch_pdl<paged_append_kernel<T, D, false>>(grid, kThreads, 0, s, a)
-                       : launch_pdl<paged_append_kernel<T, D, true>>(grid, kThreads, 0, s, a);
+  int64_t blocks = (a.b.n_tokens + (int64_t)a.block_tokens - 1) / a.block_tokens;
+  if (a.block_tokens == kMaxTokens && blocks > kResident * 148) blocks = kResident * 148;  // one wave, several rounds each
+  const dim3 grid((unsigned)blocks);
+  return a.interleaved ? launch_pdl<paged_append_kernel<T, D, false>>(grid, kThreads + 32, 0, s, a)
+                       : launch_pdl<paged_append_kernel<T, D, true>>(grid, kThreads + 32, 0, s, a);
 }
 
 }  // namespace

@@ -207,7 +207,8 @@ rq_status attention(rq_paged_cache* c, int layer, const rq_paged_batch* batch, c
       // device; what is known here is the width of the table, of which
       // sequences of different lengths fill about half.
       const int64_t tail = (int64_t)batch->n_seqs * (((int64_t)batch->table_width * c->cfg.page_size + 255) / 256);
-      const int64_t front = shared_blocks * (((int64_t)prefix_len + 127) / 128);
+      const int64_t seen = window > 0 && (int64_t)window + n_sink < prefix_len ? (int64_t)window + n_sink : prefix_len;
+      const int64_t front = shared_blocks * ((seen + 127) / 128);
       int64_t x = sms * tail / (tail + front);
       if (x < 1) x = 1;
       if (x > sms - c->cfg.n_kv_heads) x = sms - c->cfg.n_kv_heads;  // one CTA a head for the prefix
