@@ -365,7 +365,7 @@ rq_status rq_decode_noalloc_read_status(int* device_status);
  * length outside [0, table_width * page_size], a position outside the table
  * of angles, offsets outside [0, n_tokens] -- is not followed: the token is
  * neither written nor seen, and the call's status word becomes
- * RQ_ERR_DEVICE_INDEX (table entries of pages that no query sees are not
+ * RQ_ERR_DEVICE_INDEX, until the caller clears it (table entries of pages that no query sees are not
  * looked at). */
 typedef struct {
   int n_layers;   /* >= 1 */
@@ -447,7 +447,8 @@ rq_status rq_paged_workspace_bytes(const rq_paged_cache* cache, int n_seqs, int 
  *   and rounded once; 0 for a query that sees nothing.  Query head h reads kv
  *   head h / G.  What lies in the pages at tokens that no query of the
  *   sequence sees (behind its end, before its window) does not matter, NaN
- *   included.
+ *   included; a value that is not finite and that some query of the call sees
+ *   may reach the results of the call's other queries.
  * q: [n_tokens][n_q_heads][head_dim], tokens q_stride elements apart.  out:
  *   contiguous, same type.  lse: nullable fp32 [n_tokens][n_q_heads], the
  *   natural logarithm of the denominator (-inf where nothing is seen), with

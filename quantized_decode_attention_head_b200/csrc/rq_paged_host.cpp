@@ -60,9 +60,10 @@ rq_status fill_batch(const rq_paged_cache* c, int layer, const rq_paged_batch* b
 bool good_stride(int64_t stride, int heads, int d) { return stride >= (int64_t)heads * d && stride % 8 == 0; }
 
 // Workspace: status word at its start, then, from the next multiple of 256
-// bytes that leaves room for it: counters, the decode kernel's partial states.  The
-// offsets do not depend on the batch, so calls of different batches may share
-// a workspace one after another.
+// bytes that leaves room for it: counters, the decode kernel's partial states,
+// parts of whole rows.  The counters' place does not depend on the batch (they
+// are zero between calls, all else is written before it is read), so calls of
+// different batches may share a workspace one after another.
 constexpr size_t kStatusBytes = 256;
 constexpr size_t kCounterBytes = (rq::kMaxParts * 4 + 255) / 256 * 256;
 size_t parts_bytes(const rq_paged_cache* c) {
@@ -151,7 +152,7 @@ rq_status attention(rq_paged_cache* c, int layer, const rq_paged_batch* batch, c
   if (batch->n_tokens == 0 || batch->n_seqs == 0) return RQ_OK;
   // positions are counted in 32 bits
   const int64_t most = (int64_t)prefix_len + (int64_t)batch->table_width * c->cfg.page_size;
-  if (most + batch->n_tokens > 0x7FFFFFFF) return RQ_ERR_UNSUPPORTED;
+  if (most + batch->n_tokens > 0x7FFFFFFF || (int64_t)batch->n_tokens * 8 > 0x7FFFFFFF) return RQ_ERR_UNSUPPORTED;
   if (window > most) window = 0;  // wider than any sequence
   if (n_sink > most) n_sink = (int)most;
   const rq_status pr = prepare(c);

@@ -165,6 +165,18 @@ def test_shared_prefix(shape, what, lens, prefix, window, n_sink):
     assert cache.read_status(ws) == 0
 
 
+@pytest.mark.parametrize("prefix", [0, 300])
+def test_more_sequences_than_a_block_scans(prefix):
+    """The line of work spans several blocks of 128 sequences, empty and long ones among them."""
+    lens = [((i * 37) % 150 if i % 11 else 0, 1) for i in range(300)]
+    lens[205] = (2500, 1)
+    bt = Batch(lens, 8, 2, 64, 16, BF, seed=23, prefix=prefix)
+    cache = make(bt)
+    ws = cache.make_workspace(300, bt.rows)
+    check(bt, attend(bt, cache, workspace=ws), reference(bt))
+    assert cache.read_status(ws) == 0
+
+
 @pytest.mark.parametrize("prefix", [0, 200])
 @pytest.mark.parametrize("lens", [[(70, 1), (9, 1)], [(300, 150), (20, 3), (1, 1)]])
 def test_strided_queries_padding_scale_and_layer(lens, prefix):
