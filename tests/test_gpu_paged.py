@@ -223,6 +223,39 @@ def test_bad_pages_and_lengths_are_not_seen(lens):
     assert cache.read_status(ws) == 8
 
 
+@pytest.mark.parametrize("lens", [[(40, 1), (40, 1), (40, 1)], [(60, 30), (60, 30), (60, 30)]])
+def test_offsets_out_of_order_stay_inside_the_tensors(lens):
+    """Offsets past the packed rows, negative or decreasing: flagged, rows of
+    whole sequences right, the rows behind left as they were."""
+    bt = Batch(lens, 4, 2, 64, 16, BF, seed=29)
+    cache = make(bt)
+    ws = cache.make_workspace(3, bt.rows)
+    good = attend(bt, cache, workspace=ws)
+    n = lens[0][1]
+    out = torch.full_like(good, 7.0)
+    bt.cu[2], bt.cu[3] = 5 * n, 1  # sequence 1 runs past the end, sequence 2 goes back
+    attend(bt, cache, out=out, workspace=ws)
+    assert cache.read_status(ws) == 8
+    assert torch.equal(out[:n], good[:n]) and torch.isfinite(out.float()).all()
+    new = torch.ones((bt.total, 2, 64), dtype=BF, device="cuda")
+    cache.rq_paged_append(0, new, new, bt.table, bt.kv_lens, cu_new=bt.cu)
+    assert cache.read_status() == 8
+
+
+def test_one_workspace_for_batches_of_all_kinds():
+    """A workspace made for the largest batch serves others in turn: many
+    sequences, one, prompts, a shared prefix."""
+    kinds = [([(700, 1)] * 40, 0), ([(3000, 1)], 0), ([(300, 300), (9, 1)], 0), ([(50, 1)] * 20, 600), ([(2000, 2)] * 3, 0)]
+    bts = [Batch(lens, 8, 2, 64, 32, FP, seed=31 + i, prefix=p) for i, (lens, p) in enumerate(kinds)]
+    refs = [reference(b) for b in bts]
+    caches = [make(b) for b in bts]
+    ws = caches[0].make_workspace(40, 301)
+    for _ in range(3):
+        for b, c, r in zip(bts, caches, refs):
+            check(b, attend(b, c, workspace=ws), r)
+    assert caches[0].read_status(ws) == 0
+
+
 def _held(bt, pages):
     t = bt.table[1].long().clamp(0, pages.shape[1] - 1)
     return pages[0][t].transpose(0, 1).reshape(bt.hkv, -1, bt.d)[:, :100].to(F64)
