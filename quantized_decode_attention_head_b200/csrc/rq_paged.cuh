@@ -32,6 +32,20 @@ __device__ __forceinline__ void flag_index(int* status) {
   if (status) *status = kDeviceIndex;
 }
 
+// Loads of what a caller passes.  A kernel is resident while the call before it
+// still writes (programmatic launch), and queries may be rotated in place, so
+// none of it is read-only for the life of a kernel: not through ld.global.nc,
+// which the compiler may also move above griddepcontrol.wait.  once: what one
+// launch reads once (new tokens, queries, partial states), from L2.
+template <class V>
+__device__ __forceinline__ V ld_in(const V* p) {
+  return *p;
+}
+template <class V>
+__device__ __forceinline__ V ld_once(const V* p) {
+  return __ldcg(p);
+}
+
 // Brings a tensor map into the descriptor cache.
 __device__ __forceinline__ void prefetch_map(const CUtensorMap* map) {
   asm volatile("prefetch.tensormap [%0];\n" ::"l"(map) : "memory");
@@ -75,13 +89,13 @@ struct Seq {
 };
 __device__ __forceinline__ Seq load_seq(const PagedBatch& b, int i) {
   Seq s;
-  const int len = __ldg(b.kv_lens + i);
+  const int len = ld_in(b.kv_lens + i);
   const int64_t cap64 = (int64_t)b.width << b.page_shift;
   const int cap = cap64 > 0x7FFFFFFF ? 0x7FFFFFFF : (int)cap64;
   s.len = len < 0 ? 0 : (len > cap ? cap : len);
   bool bad = s.len != len;
   if (b.cu) {
-    const int lo = __ldg(b.cu + i), hi = __ldg(b.cu + i + 1);
+    const int lo = ld_in(b.cu + i), hi = ld_in(b.cu + i + 1);
     bad |= lo < 0 || hi < lo || hi > b.n_tokens;
     s.t0 = lo < 0 ? 0 : lo;
     const int e = hi > b.n_tokens ? b.n_tokens : hi;
@@ -100,7 +114,7 @@ __device__ __forceinline__ int seq_of(const PagedBatch& b, int t) {
   int lo = 0, hi = b.n_seqs;  // first index with cu[index + 1] > t
   while (lo < hi) {
     const int mid = (lo + hi) >> 1;
-    if (__ldg(b.cu + mid + 1) > t)
+    if (ld_in(b.cu + mid + 1) > t)
       hi = mid;
     else
       lo = mid + 1;

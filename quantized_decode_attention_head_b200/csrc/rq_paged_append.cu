@@ -62,7 +62,7 @@ __device__ __forceinline__ void load_angles(const PagedAppendArgs& a, const int*
     const float4* ts = reinterpret_cast<const float4*>(a.cos_sin + (int64_t)p0 * a.rot + half + j);
 #pragma unroll
     for (int e = 0; e < N / 4; ++e) {
-      const float4 x = __ldg(tc + e), y = __ldg(ts + e);
+      const float4 x = ld_in(tc + e), y = ld_in(ts + e);
       c[4 * e] = x.x, c[4 * e + 1] = x.y, c[4 * e + 2] = x.z, c[4 * e + 3] = x.w;
       s[4 * e] = y.x, s[4 * e + 1] = y.y, s[4 * e + 2] = y.z, s[4 * e + 3] = y.w;
     }
@@ -70,8 +70,8 @@ __device__ __forceinline__ void load_angles(const PagedAppendArgs& a, const int*
 #pragma unroll
     for (int e = 0; e < N; ++e) {
       const float* t = a.cos_sin + (int64_t)pair_position(a, pos, j + e) * a.rot;
-      c[e] = __ldg(t + j + e);
-      s[e] = __ldg(t + half + j + e);
+      c[e] = ld_in(t + j + e);
+      s[e] = ld_in(t + half + j + e);
     }
   }
 }
@@ -90,12 +90,12 @@ __device__ __forceinline__ Place place_of(const PagedAppendArgs& a, int64_t t64)
 #pragma unroll
     for (int k = 0; k < kMaxAxes; ++k)
       if (k < a.n_axes) {
-        o.pos[k] = a.positions ? __ldg(a.positions + (int64_t)k * a.b.n_tokens + t) : at;
+        o.pos[k] = a.positions ? ld_in(a.positions + (int64_t)k * a.b.n_tokens + t) : at;
         if ((unsigned)o.pos[k] >= (unsigned)a.n_positions) o.state = 2;
       }
   }
   if (at >= 0) {
-    o.row = page_row(a.b, __ldg(a.b.table + (int64_t)seq * a.b.width + (at >> a.b.page_shift)));
+    o.row = page_row(a.b, ld_in(a.b.table + (int64_t)seq * a.b.width + (at >> a.b.page_shift)));
     if (o.row >= 0) o.row += at & ((1 << a.b.page_shift) - 1);
   }
   if (at < 0 || o.state == 2) flag_index(a.b.status);
@@ -166,8 +166,8 @@ __device__ __forceinline__ void move_tokens(const PagedAppendArgs& a, const Plac
       const int h = h0 + i * groups;
       if (h < heads) {
         const uint16_t* src = source(h);
-        lo[i] = __ldg(reinterpret_cast<const uint4*>(src) + first);
-        if (paired) hi[i] = __ldg(reinterpret_cast<const uint4*>(src + half) + first);
+        lo[i] = ld_once(reinterpret_cast<const uint4*>(src) + first);
+        if (paired) hi[i] = ld_once(reinterpret_cast<const uint4*>(src + half) + first);
       }
     }
 #pragma unroll

@@ -249,7 +249,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) {
           // a chunk lies in one page: pages hold a multiple of 16 tokens
           const int t = chunk_token(ahead.w, c);
-          const int64_t r = page_row(a.b, __ldg(a.b.table + (int64_t)ahead.b * a.b.width + (t >> a.b.page_shift)));
+          const int64_t r = page_row(a.b, ld_in(a.b.table + (int64_t)ahead.b * a.b.width + (t >> a.b.page_shift)));
           uint64_t* bar = &tm.full[warp][put];
           tm.page_ok[warp][put] = r >= 0;
           if (r >= 0) {
@@ -291,8 +291,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint16_t* qp = a.q + (w.t0 + (r >> a.b.g_shift)) * a.q_stride + (h * G + (r & (G - 1))) * D + 2 * tig;
 #pragma unroll
       for (int ks = 0; ks < D / 16; ++ks) {
-        qf[ks][rr] = r < R ? __ldg(reinterpret_cast<const uint32_t*>(qp + 16 * ks)) : 0u;
-        qf[ks][2 + rr] = r < R ? __ldg(reinterpret_cast<const uint32_t*>(qp + 16 * ks + 8)) : 0u;
+        qf[ks][rr] = r < R ? ld_once(reinterpret_cast<const uint32_t*>(qp + 16 * ks)) : 0u;
+        qf[ks][2 + rr] = r < R ? ld_once(reinterpret_cast<const uint32_t*>(qp + 16 * ks + 8)) : 0u;
       }
     }
     float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
@@ -477,12 +477,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         auto at = [&](int k) { return k == 0 ? p0 : p1 + (int64_t)(2 * (k - 1)) * part_floats(D); };
         for (int r = warp; r < R; r += NW) {
           float M = -INFINITY, L = 0.f;
-          for (int k = lane; k < parts; k += 32) M = fmaxf(M, __ldcg(at(k) + kRows * D + 2 * r));
+          for (int k = lane; k < parts; k += 32) M = fmaxf(M, ld_once(at(k) + kRows * D + 2 * r));
 #pragma unroll
           for (int k = 16; k; k >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, k));
           const float mu = M == -INFINITY ? 0.f : M;
           for (int k = lane; k < parts; k += 32) {
-            const float2 x = __ldcg(reinterpret_cast<const float2*>(at(k) + kRows * D + 2 * r));
+            const float2 x = ld_once(reinterpret_cast<const float2*>(at(k) + kRows * D + 2 * r));
             L = fmaf(ex2(x.x - mu), x.y, L);
           }
 #pragma unroll
@@ -496,8 +496,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
           for (int k = 0; k < parts; ++k) {
-            const float4 x = __ldcg(reinterpret_cast<const float4*>(at(k) + r * D + 4 * c4));
-            const float f = ex2(__ldcg(at(k) + kRows * D + 2 * r) - mu);
+            const float4 x = ld_once(reinterpret_cast<const float4*>(at(k) + r * D + 4 * c4));
+            const float f = ex2(ld_once(at(k) + kRows * D + 2 * r) - mu);
             v.x = fmaf(f, x.x, v.x);
             v.y = fmaf(f, x.y, v.y);
             v.z = fmaf(f, x.z, v.z);

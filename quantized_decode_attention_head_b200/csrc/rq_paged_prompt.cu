@@ -372,7 +372,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             row[g] = -1;
             const int jj = j + (g << a.b.page_shift);
             if (g < per && jj < key.end) {
-              const int64_t r = page_row(a.b, __ldg(key.pages + (jj >> a.b.page_shift)));
+              const int64_t r = page_row(a.b, ld_in(key.pages + (jj >> a.b.page_shift)));
               if (r >= 0) {
                 row[g] = (int)r + head_row;
                 bytes += ps * D * 2;
@@ -435,7 +435,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               for (int i = lane; i < kKeys; i += 32) {
                 const int jj = j + i;
                 bool live = jj < key.hi && (jj >= key.lo || jj < key.sink);
-                if (live && any_bad) live = page_row(a.b, __ldg(key.pages + (jj >> a.b.page_shift))) >= 0;
+                if (live && any_bad) live = page_row(a.b, ld_in(key.pages + (jj >> a.b.page_shift))) >= 0;
                 if (!live)
 #pragma unroll
                   for (int c = 0; c < C::P * 8; ++c)
@@ -489,7 +489,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int token = sh.row_token[r];
         x[i] = make_uint4(0, 0, 0, 0);
         if (token >= 0)
-          x[i] = __ldg(reinterpret_cast<const uint4*>(a.q + token * a.q_stride + (h * G + ((row0 + r) & (G - 1))) * D) + c);
+          x[i] = ld_once(reinterpret_cast<const uint4*>(a.q + token * a.q_stride + (h * G + ((row0 + r) & (G - 1))) * D) + c);
       }
 #pragma unroll
       for (int i = 0; i < kLoads; ++i) {
@@ -502,7 +502,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int per = kKeys >> a.b.page_shift;  // pages a tile
     for (int i = tid - 128; i < n_steps * per; i += 256) {
       const int j = key_of(key, key.t0 + i / per) + ((i % per) << a.b.page_shift);
-      if (j < key.end && page_row(a.b, __ldg(key.pages + (j >> a.b.page_shift))) < 0) sh.bad = 1;
+      if (j < key.end && page_row(a.b, ld_in(key.pages + (j >> a.b.page_shift))) < 0) sh.bad = 1;
     }
     fence_proxy_async_smem();
     named_barrier();
@@ -536,7 +536,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           pages = 0;
           for (int g = 0; g < 8; ++g) {
             const int jj = j + 16 * g;
-            if (jj < key.end && page_row(a.b, __ldg(key.pages + (jj >> a.b.page_shift))) >= 0) pages |= 1u << g;
+            if (jj < key.end && page_row(a.b, ld_in(key.pages + (jj >> a.b.page_shift))) >= 0) pages |= 1u << g;
           }
         }
 #pragma unroll 1
@@ -713,7 +713,7 @@ __global__ void __launch_bounds__(128) paged_merge_kernel(const __grid_constant_
   if (few && shared == 0) return;  // the decode kernel wrote the result
   const int slots = shared + (few ? 1 : own);
   float M = -INFINITY;
-  for (int k = lane; k < slots; k += 32) M = fmaxf(M, __ldg(a.rows_ml + 2 * (k * n_rows + row)));
+  for (int k = lane; k < slots; k += 32) M = fmaxf(M, ld_once(a.rows_ml + 2 * (k * n_rows + row)));
 #pragma unroll
   for (int k = 16; k; k >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, k));
   const float mu = M == -INFINITY ? 0.f : M;
@@ -726,17 +726,17 @@ __global__ void __launch_bounds__(128) paged_merge_kernel(const __grid_constant_
 #pragma unroll 16
   for (int k = 0; k < slots; ++k) {
     const int64_t at = k * n_rows + row;
-    const float2 x = __ldg(reinterpret_cast<const float2*>(a.rows_ml + 2 * at));
+    const float2 x = ld_once(reinterpret_cast<const float2*>(a.rows_ml + 2 * at));
     const float f = ex2(x.x - mu);
     L = fmaf(f, x.y, L);
     if constexpr (E == 4) {
-      const float4 o = __ldg(reinterpret_cast<const float4*>(a.rows_o + at * D) + lane);
+      const float4 o = ld_once(reinterpret_cast<const float4*>(a.rows_o + at * D) + lane);
       v[0] = fmaf(f, o.x, v[0]);
       v[1] = fmaf(f, o.y, v[1]);
       v[2] = fmaf(f, o.z, v[2]);
       v[3] = fmaf(f, o.w, v[3]);
     } else {
-      const float2 o = __ldg(reinterpret_cast<const float2*>(a.rows_o + at * D) + lane);
+      const float2 o = ld_once(reinterpret_cast<const float2*>(a.rows_o + at * D) + lane);
       v[0] = fmaf(f, o.x, v[0]);
       v[1] = fmaf(f, o.y, v[1]);
     }
