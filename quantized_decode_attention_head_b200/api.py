@@ -6,6 +6,7 @@ librq.so.  Functions take torch tensors and pass their data pointers.
 
 from __future__ import annotations
 
+import contextlib
 import ctypes
 
 import numpy as np
@@ -22,6 +23,17 @@ def _stream_ptr(stream=None, device=None):
         return ctypes.c_void_p(stream.cuda_stream)
     idx = torch.cuda.current_device() if device is None else device
     return ctypes.c_void_p(torch._C._cuda_getCurrentRawStream(idx))
+
+
+def _allocates_on(stream):
+    """Context for what a call allocates (and reads back) itself.  Memory
+    belongs to the stream that is current when torch allocates it, and is
+    handed out again in that stream's order: so with `stream` given it has to
+    be allocated with that stream current, or other work may get a temporary
+    while the call's kernels still use it."""
+    import torch
+
+    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
 
 
 def _dptr(t):
@@ -92,11 +104,12 @@ def rq_measure_distortion(x, role, bits, stream=None):
     _check_tensor("x", x, torch.bfloat16, align=2)
     h, t, d = x.shape
     bits = np.ascontiguousarray(bits, dtype=np.int32)
-    mse = torch.empty((h, bits.size), dtype=torch.float64, device=x.device)
-    check("rq_measure_distortion", lib().rq_measure_distortion(
-        _dptr(x), h, t, d, 0 if role == "K" else 1, bits.ctypes.data_as(ctypes.POINTER(ctypes.c_int)), bits.size,
-        _dptr(mse), _stream_ptr(stream)))
-    return mse.cpu().numpy()
+    with _allocates_on(stream):
+        mse = torch.empty((h, bits.size), dtype=torch.float64, device=x.device)
+        check("rq_measure_distortion", lib().rq_measure_distortion(
+            _dptr(x), h, t, d, 0 if role == "K" else 1, bits.ctypes.data_as(ctypes.POINTER(ctypes.c_int)), bits.size,
+            _dptr(mse), _stream_ptr(stream)))
+        return mse.cpu().numpy()
 
 
 def rq_fit_distortion(bits, mse, r2_min=0.96):
@@ -232,7 +245,8 @@ class QuantizedKVCache:
         import torch
 
         nb = self.rq_decode_workspace_bytes(n_splits)
-        ws = torch.empty(nb, dtype=torch.uint8, device=self.buffer.device)
+        with _allocates_on(stream):
+            ws = torch.empty(nb, dtype=torch.uint8, device=self.buffer.device)
         check("rq_decode_workspace_init", lib().rq_decode_workspace_init(_dptr(ws), nb, _stream_ptr(stream)))
         return ws
 
@@ -244,7 +258,8 @@ class QuantizedKVCache:
             self.batch, self.n_q_heads, self.head_dim)
         _check_tensor("q", q, torch.bfloat16, shape)
         if out is None:
-            out = torch.empty(shape, dtype=torch.float32, device=q.device)
+            with _allocates_on(stream):
+                out = torch.empty(shape, dtype=torch.float32, device=q.device)
         _check_tensor("out", out, torch.float32, shape)
         if workspace is None:
             workspace = self.make_workspace(n_splits, stream)
@@ -270,7 +285,8 @@ class QuantizedKVCache:
         _check_tensor("k_new", k_new, torch.bfloat16, kshape)
         _check_tensor("v_new", v_new, torch.bfloat16, kshape)
         if out is None:
-            out = torch.empty(qshape, dtype=torch.float32, device=q.device)
+            with _allocates_on(stream):
+                out = torch.empty(qshape, dtype=torch.float32, device=q.device)
         _check_tensor("out", out, torch.float32, qshape)
         if workspace is None:
             workspace = self.make_workspace(n_splits, stream)
@@ -298,8 +314,10 @@ class PagedKVCache:
     sequence's new tokens begin among the packed ones; None: one new token
     each.  All three are CUDA tensors, read when the kernel runs.
 
-    Calls run on `stream`, or on the current stream of the pages' device.  As
-    the C handle, an object is for one thread of control.
+    Calls run on `stream`, or on the current stream of the pages' device; what
+    they allocate (results, a workspace that is not given) is memory of that
+    stream, as if it were the current one.  As the C handle, an object is for
+    one thread of control.
     """
 
     def __init__(self, k_pages, v_pages, n_q_heads):
@@ -394,6 +412,13 @@ class PagedKVCache:
             raise ValueError(f"{name} must start on a 16-byte boundary (a view at an offset into a larger tensor?)")
         return s0
 
+    def _new_like(self, q, stream):
+        """A contiguous tensor of q's type and shape, memory of `stream`."""
+        if stream is None:
+            return self._empty_like(q, memory_format=self._contiguous)
+        with _allocates_on(stream):
+            return self._empty_like(q, memory_format=self._contiguous)
+
     def _launch(self, func, fn, stream, *args):
         """Calls fn on `stream` (default: the current stream of the pages'
         device), with that device current."""
@@ -455,7 +480,7 @@ class PagedKVCache:
                 if q.shape[0] != n:
                     raise ValueError(f"q has {q.shape[0]} tokens, k_new {n}")
                 if q_out is None:
-                    q_out = self._empty_like(q, memory_format=self._contiguous)
+                    q_out = self._new_like(q, stream)
                 else:
                     _check_tensor("q_out", q_out, self.dtype, q.shape)
                     _same_device("q_out", q_out, self.device)
@@ -476,7 +501,8 @@ class PagedKVCache:
         import torch
 
         nb = self.rq_paged_workspace_bytes(n_seqs, n_tokens)
-        ws = torch.empty(nb, dtype=torch.uint8, device=self.k_pages.device)
+        with _allocates_on(stream):
+            ws = torch.empty(nb, dtype=torch.uint8, device=self.k_pages.device)
         self._launch("rq_decode_workspace_init", lib().rq_decode_workspace_init, stream, _dptr(ws), nb)
         return ws
 
@@ -514,7 +540,7 @@ class PagedKVCache:
         n = q.shape[0]
         n_seqs = self._batch(n, page_table, kv_lens, cu_new, max_new)
         if out is None:
-            out = self._empty_like(q, memory_format=self._contiguous)
+            out = self._new_like(q, stream)
         else:
             _check_tensor("out", out, self.dtype, q.shape)
             _same_device("out", out, self.device)

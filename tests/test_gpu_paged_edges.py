@@ -4,8 +4,9 @@ streams, lengths past the table, freed pages, weights of very different size."""
 import pytest
 import torch
 
-from paged_helpers import Batch, angles
-from quantized_decode_attention_head_b200 import PagedKVCache
+from paged_helpers import Batch, angles, check, reference
+from quantized_decode_attention_head_b200 import PagedKVCache, QuantizedKVCache
+from quantized_decode_attention_head_b200.api import rq_measure_distortion
 
 pytestmark = pytest.mark.gpu
 BF = torch.bfloat16
@@ -51,3 +52,80 @@ def test_rotated_in_place_and_attended_at_once(lens, prefix):
         got.append(attend(bt, cache, 500, 3, workspace=ws))
     assert all(torch.equal(a, b) for a, b in zip(got, want))
     assert cache.read_status(ws) == 0 and cache.read_status() == 0
+
+
+# ------------------------------------------------------------------ streams
+def stream_of(address):
+    """The stream whose memory the allocator counts this address to."""
+    for seg in torch.cuda.memory_snapshot():
+        if seg["address"] <= address < seg["address"] + seg["total_size"]:
+            return seg["stream"]
+    raise AssertionError("not memory of the allocator")
+
+
+def test_what_a_call_allocates_is_memory_of_its_stream():
+    bt = Batch([(900, 1), (50, 1)], 8, 4, 128, 64, BF, seed=15)
+    cache = make(bt)
+    used = []
+
+    def spy(fn):
+        def call(*args):
+            used.append(args[-3])  # the workspace
+            return fn(*args)
+        return call
+
+    cache._attention_fns = tuple(spy(f) for f in cache._attention_fns)
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    out = attend(bt, cache, stream=s)
+    assert stream_of(out.data_ptr()) == stream_of(used[-1]) == s.cuda_stream
+    new = torch.ones((2, 4, 128), dtype=BF, device="cuda")
+    q = cache.rq_paged_append(0, new, new, bt.table, bt.kv_lens, q=bt.q, cos_sin=angles(1000, 128), stream=s)
+    assert stream_of(q.data_ptr()) == s.cuda_stream
+    assert stream_of(cache.make_workspace(2, 2, stream=s).data_ptr()) == s.cuda_stream
+    torch.cuda.synchronize()
+    here = attend(bt, cache)
+    assert stream_of(here.data_ptr()) == stream_of(used[-1]) == torch.cuda.current_stream().cuda_stream
+    # the quantized cache likewise
+    old = QuantizedKVCache(1, 1, 4, 2, 64, 0, 32, 128, [[4, 4]], [[4, 4]])
+    assert stream_of(old.make_workspace(stream=s).data_ptr()) == s.cuda_stream
+    k = torch.randn((1, 1, 2, 64, 64), device="cuda").to(BF)
+    torch.cuda.synchronize()
+    old.rq_quantize_kv(k, k, stream=s)
+    qq = torch.randn((1, 4, 64), device="cuda").to(BF)
+    torch.cuda.synchronize()
+    assert stream_of(old.rq_decode_attention(0, qq, stream=s).data_ptr()) == s.cuda_stream
+    kn = k[0, :, :, 0].contiguous()
+    torch.cuda.synchronize()
+    assert stream_of(old.rq_decode_step(0, qq, kn, kn, stream=s).data_ptr()) == s.cuda_stream
+    torch.cuda.synchronize()
+
+
+def test_two_streams_without_a_workspace():
+    """Long sequences, split and counted in the workspace, on two streams in
+    turn, while the current stream takes and fills memory of the same size."""
+    bts = [Batch([(4000, 1), (50, 1)], 8, 4, 128, 64, BF, seed=s) for s in (15, 16)]
+    bts.append(Batch([(30, 1), (200, 150)], 8, 4, 128, 64, BF, seed=17, prefix=1500))
+    refs = [reference(b) for b in bts]
+    caches = [make(b) for b in bts]
+    streams = [torch.cuda.Stream() for _ in bts]
+    sizes = [c.rq_paged_workspace_bytes(2, b.rows) for c, b in zip(caches, bts)]
+    torch.cuda.synchronize()
+    outs = []
+    for _ in range(10):
+        for b, c, s, n in zip(bts, caches, streams, sizes):
+            outs.append(attend(b, c, stream=s))
+            torch.empty(n, dtype=torch.uint8, device="cuda").fill_(0xA5)
+    torch.cuda.synchronize()
+    for i, o in enumerate(outs):
+        check(bts[i % 3], o, refs[i % 3])
+
+
+def test_distortion_measured_on_another_stream():
+    x = torch.randn((3, 256, 64), generator=torch.Generator().manual_seed(1)).to(BF).cuda()
+    want = rq_measure_distortion(x, "K", [2, 4])
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(s):
+        torch.cuda._sleep(20_000_000)  # the measurement waits behind this
+    assert (rq_measure_distortion(x, "K", [2, 4], stream=s) == want).all()
