@@ -436,7 +436,9 @@ rq_status rq_paged_append(rq_paged_cache* cache, int layer, const rq_paged_batch
  * counters, partial results.  Enough for every batch of at most n_seqs
  * sequences and n_tokens packed tokens, any lengths and prefix; zero it once
  * with rq_decode_workspace_init.  Calls that share a workspace must not
- * overlap on the GPU (graphs captured with it among them). */
+ * overlap on the GPU (graphs captured with it among them).  A status word of
+ * RQ_ERR_DEVICE_TIMEOUT (which RQ_ERR_DEVICE_INDEX does not replace) means
+ * that results of a call are incomplete. */
 rq_status rq_paged_workspace_bytes(const rq_paged_cache* cache, int n_seqs, int n_tokens, size_t* bytes);
 
 /* rq_paged_attention -- attention of the batch's new tokens over the pages of

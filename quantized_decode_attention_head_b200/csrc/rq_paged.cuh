@@ -28,8 +28,19 @@ __device__ __forceinline__ bool bar_wait(uint64_t* bar, uint32_t parity) {
 // The lowest n bits (n <= 0: none, n >= 32: all).
 __device__ __forceinline__ uint32_t low_bits(int n) { return n >= 32 ? 0xFFFFFFFFu : n <= 0 ? 0u : (1u << n) - 1u; }
 
+// The status word: a wait that gave up is not hidden by an index out of range,
+// whichever comes first.
 __device__ __forceinline__ void flag_index(int* status) {
-  if (status) *status = kDeviceIndex;
+  if (status) atomicCAS(status, 0, kDeviceIndex);
+}
+__device__ __forceinline__ void flag_timeout(int* status) { atomicExch(status, kDeviceTimeout); }
+
+// After a wait that gave up: time (10 ms) for copies still in flight to land
+// before the shared memory goes to another CTA.
+__device__ __forceinline__ void let_copies_land() {
+  const uint64_t t0 = global_timer_ns();
+  while (global_timer_ns() - t0 < 10000000ull) {
+  }
 }
 
 // Loads of what a caller passes.  A kernel is resident while the call before it

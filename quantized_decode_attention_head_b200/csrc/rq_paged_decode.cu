@@ -273,7 +273,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   int get = 0;
   uint32_t phase = 0;
-  bool dead = false;  // a wait gave up
+  bool dead = false;  // a wait gave up (the whole warp's)
   const int G = 1 << a.b.g_shift;
   int64_t u = u0;
   while (u < u1 && cur.b < a.b.n_seqs) {
@@ -308,10 +308,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int c = i * NW + warp;
       if (c >= w.chunks) break;
       const int t = chunk_token(w, c);
-      if (!dead && !bar_wait(&tm.full[warp][get], phase)) {
+      if (!dead && !__all_sync(0xffffffffu, bar_wait(&tm.full[warp][get], phase))) {
+        // nothing more is copied or multiplied; the warp still counts its
+        // streams as done, so that the counters return to zero
         dead = true;
-        if (lane == 0) *a.b.status = kDeviceTimeout;
+        left = 0;
+        if (lane == 0) flag_timeout(a.b.status);
       }
+      if (dead) break;
       __syncwarp();
       uint8_t* st = ring + (warp * C::S + get) * C::STAGE;
       const uint32_t kb = smem_u32(st), vb = smem_u32(st + C::HALF);
@@ -518,6 +522,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (cur.b != b) base += seq_units;
     }
   }
+  if (dead) let_copies_land();
   if (!a.first) griddep_wait();
 }
 

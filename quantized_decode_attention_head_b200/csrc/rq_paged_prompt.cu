@@ -675,13 +675,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   tc_fence_after();
   if (sh.dead) {
-    // a wait gave up: report it, and let copies still in flight land before
-    // the shared memory goes to another CTA
+    // a wait gave up: report it
     if (tid == 0) {
-      *a.b.status = kDeviceTimeout;
-      const uint64_t t0 = global_timer_ns();
-      while (global_timer_ns() - t0 < 10000000ull) {
-      }
+      flag_timeout(a.b.status);
+      let_copies_land();
     }
     __syncthreads();
   }

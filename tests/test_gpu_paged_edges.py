@@ -1,11 +1,13 @@
 """The paged 16-bit cache on the GPU where callers leave the usual path: other
 streams, lengths past the table, freed pages, weights of very different size."""
 
+import ctypes
+
 import pytest
 import torch
 
 from paged_helpers import Batch, angles, check, reference
-from quantized_decode_attention_head_b200 import PagedKVCache, QuantizedKVCache
+from quantized_decode_attention_head_b200 import PagedKVCache, QuantizedKVCache, _lib
 from quantized_decode_attention_head_b200.api import rq_measure_distortion
 
 pytestmark = pytest.mark.gpu
@@ -129,3 +131,23 @@ def test_distortion_measured_on_another_stream():
     with torch.cuda.stream(s):
         torch.cuda._sleep(20_000_000)  # the measurement waits behind this
     assert (rq_measure_distortion(x, "K", [2, 4], stream=s) == want).all()
+
+
+# ------------------------------------------------------------------- status
+@pytest.mark.parametrize("lens,prefix", [([(100, 1), (100, 1)], 0), ([(100, 60), (100, 60)], 0), ([(40, 1)], 200)])
+def test_a_timeout_is_not_replaced_by_an_index(lens, prefix):
+    """A wait that gave up stays in the status word when a later call of the
+    workspace meets a page that does not exist."""
+    bt = Batch(lens, 4, 2, 64, 16, BF, seed=11, prefix=prefix)
+    cache = make(bt)
+    ws = cache.make_workspace(2, bt.rows)
+    bt.table[0, 1] = 1 << 30
+    attend(bt, cache, workspace=ws)
+    assert cache.read_status(ws) == 8
+    stream = ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
+    assert _lib.lib().rq_decode_workspace_init(ctypes.c_void_p(ws.data_ptr()), ws.numel(), stream) == 0
+    assert _lib.lib().rq_selftest_device_timeout(ctypes.c_void_p(ws.data_ptr()), ws.numel(), 2_000_000, stream) == 0
+    torch.cuda.synchronize()
+    assert cache.read_status(ws) == 7
+    attend(bt, cache, workspace=ws)
+    assert cache.read_status(ws) == 7
