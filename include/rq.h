@@ -366,7 +366,10 @@ rq_status rq_decode_noalloc_read_status(int* device_status);
  * of angles, offsets outside [0, n_tokens] -- is not followed: the token is
  * neither written nor seen, and the call's status word becomes
  * RQ_ERR_DEVICE_INDEX, until the caller clears it (table entries of pages that no query sees are not
- * looked at). */
+ * looked at).  Of a sequence longer than its table, what the table has room
+ * for is written and seen, and its queries stand where the length puts them;
+ * a length below zero counts as zero; a sequence whose offsets leave
+ * [0, n_tokens] has no new tokens in the call. */
 typedef struct {
   int n_layers;   /* >= 1 */
   int n_pages;    /* >= 1, of every layer */

@@ -92,11 +92,14 @@ struct Fp16 {
 };
 
 // A sequence of the batch as the device finds it: its packed tokens are
-// [t0, t0 + n), it holds len tokens.  Offsets and lengths out of range are
-// brought back into it (and flagged), so that nothing is read or written
-// outside the caller's tensors.
+// [t0, t0 + n), new token i is token end - n + i of the sequence, of which the
+// table has room for the first len.  Out of range, and flagged: a length past
+// the table (len ends there, positions stay what the length makes them), one
+// below zero (counts as zero), and offsets that leave the packed rows (no new
+// tokens).  So nothing is read or written outside the caller's tensors, nor
+// any token in another's place.
 struct Seq {
-  int t0, n, len;
+  int t0, n, len, end;
 };
 __device__ __forceinline__ Seq load_seq(const PagedBatch& b, int i) {
   Seq s;
@@ -104,13 +107,14 @@ __device__ __forceinline__ Seq load_seq(const PagedBatch& b, int i) {
   const int64_t cap64 = (int64_t)b.width << b.page_shift;
   const int cap = cap64 > 0x7FFFFFFF ? 0x7FFFFFFF : (int)cap64;
   s.len = len < 0 ? 0 : (len > cap ? cap : len);
+  s.end = len < 0 ? 0 : (len > b.top ? b.top : len);
   bool bad = s.len != len;
   if (b.cu) {
     const int lo = ld_in(b.cu + i), hi = ld_in(b.cu + i + 1);
-    bad |= lo < 0 || hi < lo || hi > b.n_tokens;
-    s.t0 = lo < 0 ? 0 : lo;
-    const int e = hi > b.n_tokens ? b.n_tokens : hi;
-    s.n = e > s.t0 ? e - s.t0 : 0;
+    const bool out = lo < 0 || hi < lo || hi > b.n_tokens;
+    bad |= out;
+    s.t0 = out ? 0 : lo;
+    s.n = out ? 0 : hi - lo;
   } else {
     s.t0 = i;
     s.n = 1;

@@ -24,6 +24,7 @@ struct PagedBatch {
   int n_pages, page_shift;  // page_size = 1 << page_shift
   int hq, hkv, g_shift;     // G = 1 << g_shift
   int64_t page_base;        // rows before the layer's first page
+  int top;                  // lengths are counted up to here: every position stays below 2^31
   int* status;              // nullable in appends
 };
 

@@ -84,7 +84,7 @@ __device__ __forceinline__ Place place_of(const PagedAppendArgs& a, int64_t t64)
   if (seq < 0) return o;
   const Seq s = load_seq(a.b, seq);
   if (t < s.t0 || t >= s.t0 + s.n) return o;  // offsets out of order: the token has no sequence
-  const int at = s.len - s.n + (t - s.t0);
+  const int at = s.end - s.n + (t - s.t0);
   o.state = 1;
   if (a.cos_sin) {
 #pragma unroll
@@ -94,7 +94,7 @@ __device__ __forceinline__ Place place_of(const PagedAppendArgs& a, int64_t t64)
         if ((unsigned)o.pos[k] >= (unsigned)a.n_positions) o.state = 2;
       }
   }
-  if (at >= 0) {
+  if (at >= 0 && at < s.len) {
     o.row = page_row(a.b, ld_in(a.b.table + (int64_t)seq * a.b.width + (at >> a.b.page_shift)));
     if (o.row >= 0) o.row += at & ((1 << a.b.page_shift) - 1);
   }

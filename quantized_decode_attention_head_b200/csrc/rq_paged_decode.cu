@@ -73,6 +73,7 @@ struct Team {
 // queries sees are, in order, chunks [0, ns) (first tokens) and [lo_c, ...).
 struct Walk {
   int t0, n, len;      // packed tokens, tokens held
+  int first;           // place of the first query in the sequence
   int lo, sink;        // tokens [0, sink) and [lo, len) are seen by some query
   int ns, lo_c, chunks, units;
 };
@@ -84,8 +85,8 @@ __device__ __noinline__ Walk walk_of(const PagedAttnArgs& a, int b) {
   w.t0 = s.t0;
   w.n = s.n;
   w.len = s.len;
-  const int first = a.prefix_len + s.len - s.n;  // position of the first query
-  int lo = a.window > 0 ? first + 1 - a.window - a.prefix_len : 0;
+  w.first = s.end - s.n;
+  int lo = a.window > 0 ? w.first + 1 - a.window : 0;
   lo = lo < 0 ? 0 : (lo > s.len ? s.len : lo);
   int sink = a.window > 0 ? a.n_sink - a.prefix_len : 0;
   sink = sink < 0 ? 0 : (sink > s.len ? s.len : sink);
@@ -301,7 +302,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int c = 0; c < D / 8; ++c)
 #pragma unroll
       for (int e = 0; e < 4; ++e) o[c][e] = 0.f;
-    const int p_first = w.len - w.n;  // local positions (the prefix left out)
+    const int p_first = w.first;  // local positions (the prefix left out)
     const int p_row[2] = {p_first + (gid >> a.b.g_shift), p_first + ((gid + 8) >> a.b.g_shift)};
 
     for (int i = i_begin; i < i_end; ++i) {

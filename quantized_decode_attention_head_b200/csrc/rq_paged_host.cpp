@@ -53,6 +53,7 @@ rq_status fill_batch(const rq_paged_cache* c, int layer, const rq_paged_batch* b
   o.hq = c->cfg.n_q_heads;
   o.hkv = c->cfg.n_kv_heads;
   o.g_shift = c->g_shift;
+  o.top = 0x7FFFFFFF;
   o.page_base = (int64_t)layer * c->cfg.n_pages * c->cfg.n_kv_heads * c->cfg.page_size;
   return RQ_OK;
 }
@@ -153,6 +154,7 @@ rq_status attention(rq_paged_cache* c, int layer, const rq_paged_batch* batch, c
   // positions are counted in 32 bits
   const int64_t most = (int64_t)prefix_len + (int64_t)batch->table_width * c->cfg.page_size;
   if (most + batch->n_tokens > 0x7FFFFFFF || (int64_t)batch->n_tokens * 8 > 0x7FFFFFFF) return RQ_ERR_UNSUPPORTED;
+  a.b.top = 0x7FFFFFFF - prefix_len - batch->n_tokens;
   if (window > most) window = 0;  // wider than any sequence
   if (n_sink > most) n_sink = (int)most;
   const rq_status pr = prepare(c);

@@ -215,7 +215,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   // ---- which rows
   int row0 = 0, rows = 0;
-  Seq seq = {0, 0, 0};
+  Seq seq = {};
   if (a.over_prefix) {
     row0 = blockIdx.x * kBlockRows;
     rows = a.b.n_tokens << a.b.g_shift;
@@ -292,14 +292,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (b >= 0) {
           const Seq s = load_seq(a.b, b);
           if (token >= s.t0 && token < s.t0 + s.n)
-            p = a.prefix_len + s.len - s.n + (token - s.t0);
+            p = a.prefix_len + s.end - s.n + (token - s.t0);
           else
             token = -1;
         } else {
           token = -1;
         }
       } else {
-        p = a.prefix_len + seq.len - seq.n + token;
+        p = a.prefix_len + seq.end - seq.n + token;
         token += seq.t0;
       }
     }
@@ -703,7 +703,7 @@ __global__ void __launch_bounds__(128) paged_merge_kernel(const __grid_constant_
   }
   const int token = (int)(row / a.b.hq);
   const int b = seq_of(a.b, token);
-  const Seq s = b >= 0 ? load_seq(a.b, b) : Seq{0, 0, 0};
+  const Seq s = b >= 0 ? load_seq(a.b, b) : Seq{};
   griddep_wait();
   if (token < s.t0 || token >= s.t0 + s.n) return;  // no sequence's
   const bool few = a.few_rows_apart && (s.n << a.b.g_shift) <= kDecodeRows;

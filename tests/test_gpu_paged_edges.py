@@ -2,11 +2,12 @@
 streams, lengths past the table, freed pages, weights of very different size."""
 
 import ctypes
+import math
 
 import pytest
 import torch
 
-from paged_helpers import Batch, angles, check, reference
+from paged_helpers import F64, Batch, angles, check, reference, rotate
 from quantized_decode_attention_head_b200 import PagedKVCache, QuantizedKVCache, _lib
 from quantized_decode_attention_head_b200.api import rq_measure_distortion
 
@@ -151,3 +152,100 @@ def test_a_timeout_is_not_replaced_by_an_index(lens, prefix):
     assert cache.read_status(ws) == 7
     attend(bt, cache, workspace=ws)
     assert cache.read_status(ws) == 7
+
+
+# ----------------------------------------------------- lengths and offsets
+@pytest.mark.parametrize("positions", [False, True])
+def test_append_past_the_table_keeps_what_is_there(positions):
+    """Lengths past the table, and far from it: tokens whose place lies in the
+    table are written there, the others nowhere."""
+    bt = Batch([(32, 1), (32, 5), (32, 3), (20, 2), (32, 2), (32, 2)], 4, 2, 64, 16, BF, seed=51)
+    lens = [33, 35, 40, 20, 2**31 - 1, -(2**31)]
+    bt.kv_lens.copy_(torch.tensor(lens, dtype=torch.int32))
+    g = torch.Generator().manual_seed(52)
+    k, v = (torch.randn((bt.total, 2, 64), generator=g).to(BF).cuda() for _ in range(2))
+    cs = angles(64, 64)
+    kw = dict(positions=torch.arange(bt.total, dtype=torch.int32, device="cuda")) if positions else {}
+    want_k, want_v = bt.k_pages.clone(), bt.v_pages.clone()
+    want_q = torch.zeros_like(bt.q)
+    t = 0
+    for b, (_, n) in enumerate(bt.lens):
+        for i in range(n):
+            at = lens[b] - n + i
+            p = t if positions else at
+            if 0 <= p < 64:
+                c, s = cs[p, :32][None], cs[p, 32:][None]
+                want_q[t] = rotate(bt.q[t : t + 1], c, s, False, 64).to(BF)[0]
+                if 0 <= at < 32:
+                    page = int(bt.table[b, at // 16])
+                    want_k[0, page, :, at % 16] = rotate(k[t : t + 1], c, s, False, 64).to(BF)[0]
+                    want_v[0, page, :, at % 16] = v[t]
+            t += 1
+    cache = make(bt)
+    q = cache.rq_paged_append(0, k, v, bt.table, bt.kv_lens, cu_new=bt.cu, q=bt.q, cos_sin=cs, **kw)
+    assert cache.read_status() == 8
+    assert torch.equal(bt.k_pages, want_k) and torch.equal(bt.v_pages, want_v) and torch.equal(q, want_q)
+
+
+@pytest.mark.parametrize("n", [1, 5, 40])
+@pytest.mark.parametrize("window,n_sink", [(0, 0), (30, 3)])
+@pytest.mark.parametrize("prefix", [0, 150])
+def test_attention_past_the_table_sees_what_is_there(n, window, n_sink, prefix):
+    """A length past the table: its queries stand where the length puts them
+    and see the keys that the table holds; other sequences are as ever."""
+    bt = Batch([(64, n), (64, n)], 4, 2, 64, 16, BF, seed=53, prefix=prefix)
+    bt.kv_lens[1] = 64 + 7
+    cache = make(bt)
+    ws = cache.make_workspace(2, bt.rows)
+    got = attend(bt, cache, window, n_sink, workspace=ws)
+    assert cache.read_status(ws) == 8
+    k, v = bt.held(bt.k_pages, 1), bt.held(bt.v_pages, 1)
+    p = prefix + 71 - n + torch.arange(n, device="cuda")[:, None]
+    j = torch.arange(prefix + 64, device="cuda")
+    see = j <= p
+    if window:
+        see &= (p - j < window) | (j < n_sink)
+    for h in range(4):
+        x = (bt.q[n:, h].to(F64) @ k[h // 2].T / 8.0).masked_fill(~see, -math.inf)
+        w = torch.softmax(x, 1)
+        # one rounding of each weight and one of the result (2^-8 each), sums and exponentials far below
+        tol = 2.0**-8 * 1.01 * (w @ v[h // 2]).abs() + 2.0**-8 * 1.01 * (w @ v[h // 2].abs())
+        assert ((got[n:, h].to(F64) - w @ v[h // 2]).abs() <= tol).all(), h
+    bt.kv_lens[1] = 64
+    same = attend(bt, cache, window, n_sink, workspace=ws)
+    assert torch.equal(got[:n], same[:n])
+    # as far as a length goes, and below zero
+    bt.kv_lens[1] = 2**31 - 1
+    far = attend(bt, cache, 0, 0, workspace=ws)
+    bt.kv_lens[1] = -(2**31)
+    none = attend(bt, cache, window, n_sink, workspace=ws)
+    bt.kv_lens[1] = 64 + n
+    every = attend(bt, cache, 0, 0, workspace=ws)
+    assert torch.equal(far[n:], every[n:]) and torch.equal(none[:n], same[:n])
+    assert prefix or (none[n:] == 0).all()
+
+
+@pytest.mark.parametrize("n", [2, 40])
+@pytest.mark.parametrize("cu,bad", [([0, 1, 2, 4], 2), ([-1, 1, 2, 3], 0)])
+def test_a_sequence_whose_offsets_leave_the_rows_has_no_new_tokens(n, cu, bad):
+    """Offsets in units of n rows of three sequences, one reaching outside:
+    nothing of it is written, the others are as ever."""
+    bt = Batch([(60, n)] * 3, 4, 2, 64, 16, BF, seed=55)
+    cache = make(bt)
+    ws = cache.make_workspace(3, bt.rows)
+    good = attend(bt, cache, workspace=ws)
+    bt.cu.copy_(torch.tensor([n * x for x in cu], dtype=torch.int32))
+    out = torch.full_like(good, 7.0)
+    attend(bt, cache, out=out, workspace=ws)
+    assert cache.read_status(ws) == 8
+    for b in range(3):
+        rows = slice(b * n, b * n + n)
+        assert torch.equal(out[rows], good[rows]) if b != bad else (out[rows] == 7.0).all()
+    new = torch.ones((bt.total, 2, 64), dtype=BF, device="cuda")
+    before = bt.k_pages.clone()
+    cache.rq_paged_append(0, new, new, bt.table, bt.kv_lens, cu_new=bt.cu)
+    assert cache.read_status() == 8
+    for b in range(3):
+        pages = bt.table[b].long()
+        same = (bt.k_pages[0, pages] == before[0, pages]).all()
+        assert bool(same) == (b == bad)
