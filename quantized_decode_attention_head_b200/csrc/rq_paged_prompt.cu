@@ -186,6 +186,12 @@ struct Keys {
   int lo, hi, sink;  // keys [lo, hi) and [0, sink) are seen by some row
   int ns, lo_t, t0, t1;
   const int* pages;
+  // Does some row see a key of the page (of ps keys) that begins at key j?
+  // Other pages are not looked up, though a tile may reach over them: they may
+  // have been freed.
+  __device__ __forceinline__ bool needs(int j, int ps) const {
+    return j < sink || (j < hi && j > lo - ps && lo < hi);
+  }
 };
 __device__ __forceinline__ int key_of(const Keys& k, int tile) {
   return kKeys * (tile < k.ns ? tile : k.lo_t + tile - k.ns);
@@ -371,7 +377,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int g = 0; g < 8; ++g) {
             row[g] = -1;
             const int jj = j + (g << a.b.page_shift);
-            if (g < per && jj < key.end) {
+            if (g < per && key.needs(jj, ps)) {
               const int64_t r = page_row(a.b, ld_in(key.pages + (jj >> a.b.page_shift)));
               if (r >= 0) {
                 row[g] = (int)r + head_row;
@@ -502,7 +508,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int per = kKeys >> a.b.page_shift;  // pages a tile
     for (int i = tid - 128; i < n_steps * per; i += 256) {
       const int j = key_of(key, key.t0 + i / per) + ((i % per) << a.b.page_shift);
-      if (j < key.end && page_row(a.b, ld_in(key.pages + (j >> a.b.page_shift))) < 0) sh.bad = 1;
+      if (key.needs(j, 1 << a.b.page_shift) && page_row(a.b, ld_in(key.pages + (j >> a.b.page_shift))) < 0) sh.bad = 1;
     }
     fence_proxy_async_smem();
     named_barrier();
@@ -531,12 +537,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (__any_sync(0xffffffffu, !whole)) {
         // masked in place, 32 columns at a time: a CTA meets one to three such
         // tiles, and code unrolled over 128 columns cost more to fetch than to run
-        uint32_t pages = 0xFFu;  // bit g: the page of keys 16 g.. of the tile exists
+        uint32_t pages = 0xFFu;  // bit g: the page of keys 16 g.. of the tile was loaded
         if (any_bad) {
           pages = 0;
           for (int g = 0; g < 8; ++g) {
             const int jj = j + 16 * g;
-            if (jj < key.end && page_row(a.b, ld_in(key.pages + (jj >> a.b.page_shift))) >= 0) pages |= 1u << g;
+            const int first = jj >> a.b.page_shift << a.b.page_shift;
+            if (key.needs(first, 1 << a.b.page_shift) && page_row(a.b, ld_in(key.pages + (jj >> a.b.page_shift))) >= 0) pages |= 1u << g;
           }
         }
 #pragma unroll 1

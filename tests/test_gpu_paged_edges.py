@@ -7,7 +7,7 @@ import math
 import pytest
 import torch
 
-from paged_helpers import F64, Batch, angles, check, reference, rotate
+from paged_helpers import F64, Batch, angles, check, check_lse, reference, rotate
 from quantized_decode_attention_head_b200 import PagedKVCache, QuantizedKVCache, _lib
 from quantized_decode_attention_head_b200.api import rq_measure_distortion
 
@@ -249,3 +249,37 @@ def test_a_sequence_whose_offsets_leave_the_rows_has_no_new_tokens(n, cu, bad):
         pages = bt.table[b].long()
         same = (bt.k_pages[0, pages] == before[0, pages]).all()
         assert bool(same) == (b == bad)
+
+
+# -------------------------------------------------------------- freed pages
+def free_unseen(bt, window, n_sink):
+    """Table entries of pages that no query of the sequence sees become page
+    numbers that do not exist; those of the prefix where no sequence does."""
+    pre = torch.zeros(len(bt.prefix_pages), dtype=torch.bool)
+    for b, (kv, n) in enumerate(bt.lens):
+        seen = bt.seen(b, window, n_sink).any(0).cpu() if n else torch.zeros(bt.prefix + kv, dtype=torch.bool)
+        for j in torch.nonzero(seen[: bt.prefix]).flatten().tolist():
+            pre[j // bt.page] = True
+        own = seen[bt.prefix :]
+        for i in range(-(-kv // bt.page)):
+            if not own[i * bt.page : (i + 1) * bt.page].any():
+                bt.table[b, i] = -1 if i % 2 else 1 << 30
+    bt.prefix_pages[~pre.to(bt.prefix_pages.device)] = -7
+
+
+@pytest.mark.parametrize("lens,prefix", [
+    ([(700, 1), (300, 2), (40, 1)], 0), ([(700, 200), (555, 90), (129, 129)], 0), ([(1000, 300)], 0),
+    ([(90, 1), (40, 1)], 1000), ([(333, 120), (40, 40), (9, 1)], 700)])
+@pytest.mark.parametrize("window,n_sink", [(100, 0), (70, 4), (33, 130), (1, 0), (1, 17), (400, 20)])
+@pytest.mark.parametrize("page,d", [(16, 64), (32, 128), (64, 64)])
+def test_pages_freed_behind_the_window(lens, prefix, window, n_sink, page, d):
+    bt = Batch(lens, 8, 2, d, page, BF, seed=61 + page, prefix=prefix)
+    ref = reference(bt, window, n_sink)
+    bt.poison(window, n_sink)
+    free_unseen(bt, window, n_sink)
+    cache = make(bt)
+    lse = torch.empty((bt.rows, 8), device="cuda")
+    ws = cache.make_workspace(len(lens), bt.rows)
+    check(bt, attend(bt, cache, window, n_sink, lse=lse, workspace=ws), ref)
+    check_lse(bt, lse, ref)
+    assert cache.read_status(ws) == 0
