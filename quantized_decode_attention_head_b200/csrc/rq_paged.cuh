@@ -63,8 +63,16 @@ __device__ __forceinline__ void prefetch_map(const CUtensorMap* map) {
 }
 
 // 16-bit element types of the pages: conversions to and from fp32.
+// Weights enter the second product in the type, as powers of two relative to
+// the row's running maximum.  bf16 has fp32's exponents; fp16 ends at 2^-24,
+// and its weights are held 2^kUp (two terms) or 2^kUpLag (one term, with a
+// maximum that lags by up to 2^kLag) larger, which the sums and the stored
+// maximum share, so that what a long tail adds to the sum it adds to the
+// product too: the largest is 2^14, the smallest step 2^-38 or, in one term,
+// 2^-34 of it.
 struct Bf16 {
   static constexpr int kType = 1;  // of tcgen05 instruction descriptors
+  static constexpr float kUp = 0.f, kUpLag = 0.f, kLag = 8.f;
   static __device__ __forceinline__ float2 unpack(uint32_t u) {
     return make_float2(__uint_as_float(u << 16), __uint_as_float(u & 0xFFFF0000u));
   }
@@ -75,6 +83,7 @@ struct Bf16 {
 };
 struct Fp16 {
   static constexpr int kType = 0;
+  static constexpr float kUp = 14.f, kUpLag = 10.f, kLag = 4.f;
   static __device__ __forceinline__ float2 unpack(uint32_t u) {
     return __half22float2(*reinterpret_cast<const __half2*>(&u));
   }

@@ -21,9 +21,10 @@
 // results do not depend on timing.
 //
 // Products run on mma.sync m16n8k16 (rows = token, head), fp32 accumulation;
-// the weights enter the second product as two 16-bit terms (high and rest,
-// 2^-16 relative or better), which costs tensor issue slots that a stream of
-// memory leaves idle and keeps their rounding out of the result.
+// the weights enter the second product as two 16-bit terms (high and rest:
+// 2^-16 relative or better; fp16: or 2^-39 of the row's largest weight), which
+// costs tensor issue slots that a stream of memory leaves idle and keeps their
+// rounding out of the result.
 //
 // Measured (32/8 heads, D = 128, bf16): 64 ragged sequences up to 8192 tokens
 // 141 us, 5.8 TB/s; one of 131072 tokens 94 us, 5.7 TB/s; 16 with a window of
@@ -374,7 +375,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int nb = 0; nb < 2; ++nb) mx = fmaxf(mx, fmaxf(s[nb][2 * rr], s[nb][2 * rr + 1]));
         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-        const float mn = fmaxf(m[rr], mx * a.scale_log2);
+        const float mn = fmaxf(m[rr], fmaf(mx, a.scale_log2, -T::kUp));
         const float mu = mn == -INFINITY ? 0.f : mn;  // nothing seen yet: weights become 0
         const float alpha = ex2(m[rr] - mu);
         m[rr] = mn;

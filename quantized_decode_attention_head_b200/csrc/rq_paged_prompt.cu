@@ -13,8 +13,11 @@
 // tiles, so one tile's products run while the other's weights are computed.
 // P_t overwrites S_t (16-bit pairs, half its columns).  TMEM columns:
 // [S_0 | S_1 | O_0 | O_1].  The running maximum moves only when a row's scores
-// exceed it by 2^8 (a weight then stays below 256, exact in the type's
-// exponent), so O is rarely rescaled; sums are fp32 of the unrounded weights.
+// exceed it by 2^8 (fp16: 2^4), so O is rarely rescaled.  Weights are rounded
+// once to 16 bits, half a step of the type, where they enter the product: a
+// second term would fit the columns that P leaves free, but adds half of all
+// tensor work and more TMEM traffic, which bound the kernel.  Their sums are
+// fp32 of the unrounded weights.
 //
 // Bound.  At D = 128 a step (256 rows, 128 keys) is 2048 clocks of tensor work
 // and as many of exponentials (16 a clock an SM).  Measured (8192-token prompt,
@@ -575,8 +578,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         mx4[c] = fmaxf(mx4[c], __uint_as_float(s[c][31]));
       }
       float mx = fmaxf(max3(mx4[0], mx4[1], mx4[2]), mx4[3]);
-      mx *= a.scale_log2;
-      const bool move = mx > m + 8.0f;  // true at the first score of a row (m = -inf)
+      mx = fmaf(mx, a.scale_log2, -T::kUpLag);
+      const bool move = mx > m + T::kLag;  // true at the first score of a row (m = -inf)
       if (__any_sync(0xffffffffu, move)) {
         const float mn = move ? mx : m;
         const float alpha = move ? ex2(m - mn) : 1.f;

@@ -12,7 +12,7 @@ from quantized_decode_attention_head_b200 import PagedKVCache, QuantizedKVCache,
 from quantized_decode_attention_head_b200.api import rq_measure_distortion
 
 pytestmark = pytest.mark.gpu
-BF = torch.bfloat16
+BF, FP = torch.bfloat16, torch.float16
 
 
 def make(bt):
@@ -283,3 +283,66 @@ def test_pages_freed_behind_the_window(lens, prefix, window, n_sink, page, d):
     check(bt, attend(bt, cache, window, n_sink, lse=lse, workspace=ws), ref)
     check_lse(bt, lse, ref)
     assert cache.read_status(ws) == 0
+
+
+# ----------------------------------------------- weights of very different size
+@pytest.mark.parametrize("keys,new,prefix,seqs", [
+    (131072, 1, 0, 1), (40000, 3, 0, 1), (2000, 1, 0, 400), (40000, 40, 0, 1), (20, 1, 30000, 3), (300, 90, 20000, 1)])
+@pytest.mark.parametrize("below", [20.0, 25.6, 28.0])
+def test_one_key_outweighs_a_long_tail_in_fp16(keys, new, prefix, seqs, below):
+    """The first key's weight is about 2^below times that of any other: the
+    others count in the sum, so they have to count in the product.  With many
+    sequences (the same pages for all) no sequence's keys are divided among
+    blocks, so that one running maximum holds for most of them.
+
+    Weights are held to 2^-11 relative (twice that far in two terms), or to
+    2^-35 of the largest where that is more; the result is rounded once.
+    Scores and exponentials add 2^-17 (68 products of at most 2^5 at 2^-23)."""
+    d, hq, hkv = 64, 4, 2
+    bt = Batch([(keys, new)], hq, hkv, d, 64, FP, seed=71, prefix=prefix)
+    g = torch.Generator().manual_seed(72)
+    total = prefix + keys
+    bt.table = bt.table.expand(seqs, -1).contiguous()
+    bt.kv_lens = bt.kv_lens.expand(seqs).contiguous()
+    bt.cu = torch.arange(0, (seqs + 1) * new, new, dtype=torch.int32, device="cuda")
+    bt.q = bt.q.repeat(seqs, 1, 1)
+    # q = 4 e_0 plus a little in channel 1; key 0 has its score in channel 0, the others none there
+    bt.q.zero_()
+    bt.q[..., 0] = 4.0
+    bt.q[..., 1] = 0.25 * torch.rand((seqs * new, hq), generator=g).to(FP).cuda()
+    top = below * math.log(2.0) / 4.0 * 8.0  # scale 1/8: the score is below * ln 2
+    k = torch.zeros((hkv, total, d), dtype=FP)
+    k[:, :, 1] = torch.randn((hkv, total), generator=g).to(FP)
+    k[:, 0] = 0.0
+    k[:, 0, 0] = top
+    v = 0.5 + torch.rand((hkv, total, d), generator=g)
+    v[:, 0] = torch.randn((hkv, d), generator=g) * 2.0**-12
+    v = v.to(FP)
+    for pages, rows in ((bt.k_pages, k), (bt.v_pages, v)):
+        place(bt, pages, rows)
+    lse = torch.empty((seqs * new, hq), device="cuda")
+    cache = make(bt)
+    got = attend(bt, cache, lse=lse).to(F64)
+    k, v = k.cuda().to(F64), v.cuda().to(F64)
+    p = total - new + torch.arange(new, device="cuda")[:, None]
+    see = (torch.arange(total, device="cuda") <= p).repeat(seqs, 1)
+    for h in range(hq):
+        x = (bt.q[:, h].to(F64) @ k[h // 2].T / 8.0).masked_fill(~see, -math.inf)
+        w = torch.softmax(x, 1)
+        out, a = w @ v[h // 2], w @ v[h // 2].abs()
+        tol = 2.0**-11 * 1.01 * (out.abs() + a) + 2.0**-17 * a + total * 2.0**-35 * 1.5 + 2.0**-25
+        err = (got[:, h] - out).abs()
+        assert (err <= tol).all(), f"{float((err / tol).max()):.2f} times the tolerance"
+        assert ((lse[:, h].to(F64) - torch.logsumexp(x, 1)).abs() <= 2.0**-17).all()
+
+
+def place(bt, pages, rows):
+    """rows [kv heads, prefix + keys, d] of the batch's only sequence, into its pages."""
+    pre, own = rows[:, : bt.prefix], rows[:, bt.prefix :]
+    for part, numbers in ((pre, bt.prefix_pages), (own, bt.table[0])):
+        n = part.shape[1]
+        if n:
+            full = torch.zeros((bt.hkv, -(-n // bt.page) * bt.page, bt.d), dtype=rows.dtype)
+            full[:, :n] = part
+            blocks = full.view(bt.hkv, -1, bt.page, bt.d).transpose(0, 1)
+            pages[0, numbers[: blocks.shape[0]].long()] = blocks.to(pages.device)
