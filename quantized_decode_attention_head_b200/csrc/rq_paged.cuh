@@ -47,7 +47,9 @@ __device__ __forceinline__ void let_copies_land() {
 // still writes (programmatic launch), and queries may be rotated in place, so
 // none of it is read-only for the life of a kernel: not through ld.global.nc,
 // which the compiler may also move above griddepcontrol.wait.  once: what one
-// launch reads once (new tokens, queries, partial states), from L2.
+// launch reads once (new tokens, partial states, whole rows of queries), from
+// L2; the decode kernel reads a query's words four warps at a time, through L1
+// (from L2: attend 64 ragged sequences 148 us for 142).
 template <class V>
 __device__ __forceinline__ V ld_in(const V* p) {
   return *p;

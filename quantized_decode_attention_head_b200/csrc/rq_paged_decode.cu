@@ -293,8 +293,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint16_t* qp = a.q + (w.t0 + (r >> a.b.g_shift)) * a.q_stride + (h * G + (r & (G - 1))) * D + 2 * tig;
 #pragma unroll
       for (int ks = 0; ks < D / 16; ++ks) {
-        qf[ks][rr] = r < R ? ld_once(reinterpret_cast<const uint32_t*>(qp + 16 * ks)) : 0u;
-        qf[ks][2 + rr] = r < R ? ld_once(reinterpret_cast<const uint32_t*>(qp + 16 * ks + 8)) : 0u;
+        qf[ks][rr] = r < R ? ld_in(reinterpret_cast<const uint32_t*>(qp + 16 * ks)) : 0u;
+        qf[ks][2 + rr] = r < R ? ld_in(reinterpret_cast<const uint32_t*>(qp + 16 * ks + 8)) : 0u;
       }
     }
     float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
