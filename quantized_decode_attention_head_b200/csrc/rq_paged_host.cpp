@@ -202,6 +202,8 @@ rq_status attention(rq_paged_cache* c, int layer, const rq_paged_batch* batch, c
   const bool side_by_side = prefix_len > 0 && decode && !prompt;
   if (prefix_len > 0) {
     int sms = decode_ctas(c);
+    // no query sees more of the prefix than its window and the first tokens
+    const int64_t seen = window > 0 && (int64_t)window + n_sink < prefix_len ? (int64_t)window + n_sink : prefix_len;
     if (side_by_side) {
       // The decode kernel (what follows the prefix) and the prompt kernel (the
       // prefix) run side by side, on SMs of their own: a unit of either, 128
@@ -210,7 +212,6 @@ rq_status attention(rq_paged_cache* c, int layer, const rq_paged_batch* batch, c
       // device; what is known here is the width of the table, of which
       // sequences of different lengths fill about half.
       const int64_t tail = (int64_t)batch->n_seqs * (((int64_t)batch->table_width * c->cfg.page_size + 255) / 256);
-      const int64_t seen = window > 0 && (int64_t)window + n_sink < prefix_len ? (int64_t)window + n_sink : prefix_len;
       const int64_t front = shared_blocks * ((seen + 127) / 128);
       int64_t x = sms * tail / (tail + front);
       if (x < 1) x = 1;
@@ -219,7 +220,7 @@ rq_status attention(rq_paged_cache* c, int layer, const rq_paged_batch* batch, c
       a.n_ctas = (int)x;
       sms -= (int)x;
     }
-    shared = splits_of(c, shared_blocks, prefix_len, 0, 0, 0, sms);
+    shared = splits_of(c, shared_blocks, seen, 0, 0, 0, sms);
     if (side_by_side) {
       // what the splits leave over
       const int64_t left = decode_ctas(c) - shared_blocks * c->cfg.n_kv_heads * shared;
