@@ -158,6 +158,63 @@ __device__ __forceinline__ int64_t page_row(const PagedBatch& b, int page) {
   return b.page_base + (((int64_t)page * b.hkv) << b.page_shift);
 }
 
+constexpr int kChunk = 16;      // tokens that the decode kernel copies at once (a stage)
+constexpr int kUnitChunks = 4;  // chunks of a unit, by which it divides its work
+
+// One sequence as the decode kernel walks it: the 16-token chunks that any of its
+// queries sees are, in order, chunks [0, ns) (first tokens) and [lo_c, ...).
+struct Walk {
+  int t0, n, len;      // packed tokens, tokens held
+  int first;           // place of the first query in the sequence
+  int lo, sink;        // tokens [0, sink) and [lo, len) are seen by some query
+  int ns, lo_c, chunks, units;
+};
+// (not inlined: the decode kernel's start is bound by fetching its code)
+static __device__ __noinline__ Walk walk_of(const PagedAttnArgs& a, int b) {
+  Walk w = {};
+  if (b >= a.b.n_seqs) return w;  // no units
+  const Seq s = load_seq(a.b, b);
+  w.t0 = s.t0;
+  w.n = s.n;
+  w.len = s.len;
+  w.first = s.end - s.n;
+  int lo = a.window > 0 ? w.first + 1 - a.window : 0;
+  lo = lo < 0 ? 0 : (lo > s.len ? s.len : lo);
+  int sink = a.window > 0 ? a.n_sink - a.prefix_len : 0;
+  sink = sink < 0 ? 0 : (sink > s.len ? s.len : sink);
+  w.lo = lo;
+  w.sink = sink;
+  w.lo_c = lo / kChunk;
+  const int sc = (sink + kChunk - 1) / kChunk;
+  w.ns = sc < w.lo_c ? sc : w.lo_c;
+  w.chunks = w.ns + (s.len + kChunk - 1) / kChunk - w.lo_c;
+  const bool mine = s.n > 0 && (s.n << a.b.g_shift) <= kDecodeRows;
+  if (s.n > 0 && !mine && a.few_rows_only) flag_index(a.b.status);  // more new tokens than max_new said
+  w.units = mine ? (w.chunks > kUnitChunks ? (w.chunks + kUnitChunks - 1) / kUnitChunks : 1) : 0;  // a stream that sees nothing still writes
+  return w;
+}
+
+// How the SMs are divided when the prefix (prompt kernel) and what follows it
+// (decode kernel) run side by side, from the units that the lengths on the
+// device make of the latter.  128 keys take a CTA of either about as long (1.9
+// us measured: two units of the decode kernel's two teams, or a step of 256
+// rows), so the shares go by them.  The same in every kernel of a call.
+struct Shares {
+  int splits;  // of the prefix's keys
+  int ctas;    // of the decode kernel
+};
+__device__ __forceinline__ Shares shares_of(const PagedAttnArgs& a, int64_t tail_units) {
+  Shares s = {1, a.n_ctas};
+  if (a.front_ctas >= a.n_ctas) return s;  // the prefix fills the device for a while: one after the other
+  const int x = (int)(a.n_ctas * ((float)tail_units / ((float)tail_units + a.front_units)));
+  s.splits = (a.n_ctas - x) / a.front_ctas;
+  s.splits = s.splits < 1 ? 1 : (s.splits > a.max_splits ? a.max_splits : s.splits);
+  const int left = a.n_ctas - a.front_ctas * s.splits;
+  s.ctas = x > left ? x : left;
+  if (s.ctas < 1) s.ctas = 1;
+  return s;
+}
+
 // Four channels of a row's state (v not yet divided by l, maximum m in log2
 // units): the result, or the row's partial state for the merge of the parts.
 template <class T, int D>

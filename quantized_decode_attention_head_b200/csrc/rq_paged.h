@@ -61,7 +61,13 @@ struct PagedAttnArgs {
   int over_prefix;        // prompt kernel: all rows of the batch over the prefix
   int few_rows_apart;     // sequences of at most kDecodeRows rows are the decode kernel's
   int few_rows_only;      // the call said that no sequence has more than 16 rows a kv head
-  int n_ctas;             // CTAs of the decode kernel, two teams each
+  int n_ctas;             // SMs that may run the decode kernel's CTAs, of two teams each
+  // The decode kernel runs beside the prompt kernel over the prefix (divide):
+  int divide;             // both take their shares of n_ctas SMs from the lengths (shares_of)
+  int front_ctas;         // CTAs of the prefix, not split
+  int max_splits;         // most splits of it: what its grid holds
+  float front_units;      // its units
+  int* plan;              // the splits that shares_of found, for the merge
   float* parts;           // its partial states: two slots of part_floats(D) a team
   uint32_t* counters;     // one a team: parts of the stream that begins to be split there
   float* rows_o;          // null: results go to out; else partial states of whole rows,
@@ -78,8 +84,8 @@ constexpr int kDecodeRows = 16;  // rows of a kv head that the decode kernel tak
 __host__ __device__ constexpr int part_floats(int D) { return kDecodeRows * D + 2 * kDecodeRows; }
 
 cudaError_t launch_paged_append(const PagedAppendArgs& a, int head_dim, int dtype, cudaStream_t s);
-cudaError_t launch_paged_decode(const CUtensorMap& km, const CUtensorMap& vm, const PagedAttnArgs& a, int head_dim,
-                                int dtype, cudaStream_t s);
+cudaError_t launch_paged_decode(const CUtensorMap& km, const CUtensorMap& vm, const PagedAttnArgs& a, int ctas,
+                                int head_dim, int dtype, cudaStream_t s);
 cudaError_t launch_paged_prompt(const CUtensorMap& km, const CUtensorMap& vm, const PagedAttnArgs& a, int blocks,
                                 int splits, int head_dim, int dtype, cudaStream_t s);
 // Merges slots [0, shared) and the rows' own (one of the decode kernel or `own` of the prompt kernel).

@@ -40,11 +40,11 @@
 namespace rq {
 namespace {
 
-constexpr int NW = 4;         // warps a team
+constexpr int NW = kUnitChunks;  // warps a team, a chunk of a unit each
 constexpr int kTeams = 2;     // teams a CTA
 constexpr int kThreads = kTeams * NW * 32;
-constexpr int kChunk = 16;    // tokens a stage
 constexpr int kRows = 16;     // query rows of an MMA
+static_assert(kRows == kDecodeRows, "one MMA holds a stream's rows");
 constexpr int kMergeRows = 4; // rows a team merges at once
 
 template <int D>
@@ -69,39 +69,6 @@ struct Team {
   int64_t n[2 * NW + 1];
   int v[2];
 };
-
-// One sequence as the kernel walks it: the 16-token chunks that any of its
-// queries sees are, in order, chunks [0, ns) (first tokens) and [lo_c, ...).
-struct Walk {
-  int t0, n, len;      // packed tokens, tokens held
-  int first;           // place of the first query in the sequence
-  int lo, sink;        // tokens [0, sink) and [lo, len) are seen by some query
-  int ns, lo_c, chunks, units;
-};
-// (not inlined: the kernel's start is bound by fetching its code)
-__device__ __noinline__ Walk walk_of(const PagedAttnArgs& a, int b) {
-  Walk w = {};
-  if (b >= a.b.n_seqs) return w;  // no units
-  const Seq s = load_seq(a.b, b);
-  w.t0 = s.t0;
-  w.n = s.n;
-  w.len = s.len;
-  w.first = s.end - s.n;
-  int lo = a.window > 0 ? w.first + 1 - a.window : 0;
-  lo = lo < 0 ? 0 : (lo > s.len ? s.len : lo);
-  int sink = a.window > 0 ? a.n_sink - a.prefix_len : 0;
-  sink = sink < 0 ? 0 : (sink > s.len ? s.len : sink);
-  w.lo = lo;
-  w.sink = sink;
-  w.lo_c = lo / kChunk;
-  const int sc = (sink + kChunk - 1) / kChunk;
-  w.ns = sc < w.lo_c ? sc : w.lo_c;
-  w.chunks = w.ns + (s.len + kChunk - 1) / kChunk - w.lo_c;
-  const bool mine = s.n > 0 && (s.n << a.b.g_shift) <= kRows;
-  if (s.n > 0 && !mine && a.few_rows_only) flag_index(a.b.status);  // more new tokens than max_new said
-  w.units = mine ? (w.chunks > NW ? (w.chunks + NW - 1) / NW : 1) : 0;  // a stream that sees nothing still writes
-  return w;
-}
 
 // A place on the line of units: unit i of kv head h of sequence b.
 struct Cursor {
@@ -189,7 +156,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     more += tm.n[NW + k];
   }
   const int64_t U = (block + more) * a.b.hkv;
-  const int64_t N = U < (int64_t)gridDim.x * kTeams ? U : (int64_t)gridDim.x * kTeams;
+  const int ctas = a.divide ? min(shares_of(a, block + more).ctas, (int)gridDim.x) : (int)gridDim.x;
+  const int64_t most = (int64_t)kTeams * ctas;
+  const int64_t N = U < most ? U : most;
   const int cta = blockIdx.x * kTeams + team;
   if (cta >= N) {
     griddep_wait();
@@ -529,18 +498,18 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 template <class T, int D>
-cudaError_t launch(const CUtensorMap& km, const CUtensorMap& vm, const PagedAttnArgs& a, cudaStream_t s) {
+cudaError_t launch(const CUtensorMap& km, const CUtensorMap& vm, const PagedAttnArgs& a, int ctas, cudaStream_t s) {
   static_assert(Cfg<D>::SMEM + sizeof(Team<Cfg<D>::S>) * kTeams <= 227 * 1024, "shared memory");
   static_assert(NW * Cfg<D>::S <= NW * 32, "one thread initialises each barrier");
-  return launch_pdl<paged_decode_kernel<T, D>>(dim3(a.n_ctas), kThreads, Cfg<D>::SMEM, s, km, vm, a);
+  return launch_pdl<paged_decode_kernel<T, D>>(dim3(ctas), kThreads, Cfg<D>::SMEM, s, km, vm, a);
 }
 
 }  // namespace
 
-cudaError_t launch_paged_decode(const CUtensorMap& km, const CUtensorMap& vm, const PagedAttnArgs& a, int head_dim,
-                                int dtype, cudaStream_t s) {
-  if (head_dim == 128) return dtype == 0 ? launch<Bf16, 128>(km, vm, a, s) : launch<Fp16, 128>(km, vm, a, s);
-  return dtype == 0 ? launch<Bf16, 64>(km, vm, a, s) : launch<Fp16, 64>(km, vm, a, s);
+cudaError_t launch_paged_decode(const CUtensorMap& km, const CUtensorMap& vm, const PagedAttnArgs& a, int ctas,
+                                int head_dim, int dtype, cudaStream_t s) {
+  if (head_dim == 128) return dtype == 0 ? launch<Bf16, 128>(km, vm, a, ctas, s) : launch<Fp16, 128>(km, vm, a, ctas, s);
+  return dtype == 0 ? launch<Bf16, 64>(km, vm, a, ctas, s) : launch<Fp16, 64>(km, vm, a, ctas, s);
 }
 
 }  // namespace rq

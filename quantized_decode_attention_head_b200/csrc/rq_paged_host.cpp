@@ -60,12 +60,12 @@ rq_status fill_batch(const rq_paged_cache* c, int layer, const rq_paged_batch* b
 
 bool good_stride(int64_t stride, int heads, int d) { return stride >= (int64_t)heads * d && stride % 8 == 0; }
 
-// Workspace: status word at its start, then, from the next multiple of 256
+// Workspace: status word and plan at its start, then, from the next multiple of 256
 // bytes that leaves room for it: counters, the decode kernel's partial states,
 // parts of whole rows.  The counters' place does not depend on the batch (they
 // are zero between calls, all else is written before it is read), so calls of
 // different batches may share a workspace one after another.
-constexpr size_t kStatusBytes = 256;
+constexpr size_t kStatusBytes = 256, kPlanOffset = 64;
 constexpr size_t kCounterBytes = (rq::kMaxParts * 4 + 255) / 256 * 256;
 size_t parts_bytes(const rq_paged_cache* c) {
   return (size_t)2 * rq::kMaxParts * rq::part_floats(c->cfg.head_dim) * 4;
@@ -138,7 +138,7 @@ int splits_of(const rq_paged_cache* c, int64_t blocks, int64_t keys, int window,
 rq_status attention(rq_paged_cache* c, int layer, const rq_paged_batch* batch, const int* prefix, int prefix_len,
                     const void* q, int64_t q_stride, void* out, float* lse, float softmax_scale, int window,
                     int n_sink, void* workspace, size_t ws_bytes, cudaStream_t stream) {
-  rq::PagedAttnArgs a;
+  rq::PagedAttnArgs a = {};
   const rq_status st = fill_batch(c, layer, batch, a.b);
   if (st != RQ_OK) return st;
   if (window < 0 || n_sink < 0 || prefix_len < 0 || !(softmax_scale <= 3.0e38f)) return RQ_ERR_INVALID_ARG;
@@ -200,31 +200,29 @@ rq_status attention(rq_paged_cache* c, int layer, const rq_paged_batch* batch, c
   }
   const int64_t shared_blocks = (all_rows + rq::kPromptRows - 1) / rq::kPromptRows;
   const bool side_by_side = prefix_len > 0 && decode && !prompt;
+  int decode_grid = a.n_ctas;
+  a.divide = 0;
   if (prefix_len > 0) {
-    int sms = decode_ctas(c);
     // no query sees more of the prefix than its window and the first tokens
     const int64_t seen = window > 0 && (int64_t)window + n_sink < prefix_len ? (int64_t)window + n_sink : prefix_len;
+    shared = splits_of(c, shared_blocks, seen, 0, 0, 0, a.n_ctas - side_by_side);
     if (side_by_side) {
       // The decode kernel (what follows the prefix) and the prompt kernel (the
-      // prefix) run side by side, on SMs of their own: a unit of either, 128
-      // keys of one sequence or of 256 rows, takes about as long (1.9 us
-      // measured), so the SMs are divided by the units.  Lengths are on the
-      // device; what is known here is the width of the table, of which
-      // sequences of different lengths fill about half.
-      const int64_t tail = (int64_t)batch->n_seqs * (((int64_t)batch->table_width * c->cfg.page_size + 255) / 256);
-      const int64_t front = shared_blocks * ((seen + 127) / 128);
-      int64_t x = sms * tail / (tail + front);
-      if (x < 1) x = 1;
-      if (x > sms - c->cfg.n_kv_heads) x = sms - c->cfg.n_kv_heads;  // one CTA a head for the prefix
-      if (x < 1) x = 1;
-      a.n_ctas = (int)x;
-      sms -= (int)x;
-    }
-    shared = splits_of(c, shared_blocks, seen, 0, 0, 0, sms);
-    if (side_by_side) {
-      // what the splits leave over
-      const int64_t left = decode_ctas(c) - shared_blocks * c->cfg.n_kv_heads * shared;
-      if (left > a.n_ctas) a.n_ctas = (int)left;
+      // prefix) run side by side, with grids as large as either share may be;
+      // the decode kernel's no larger than its units if all lengths were the
+      // tables'.  Where both fit there is nothing to divide (a small call: 14
+      // us for 15.5).  Else they divide the SMs by the lengths they find, and
+      // blocks left over end at once: 64 sequences behind 32768 tokens take 69
+      // us however wide the table; divided by the table's width they took 68
+      // where it was twice the lengths, 231 where it was 32 times.
+      const int64_t ctas = shared_blocks * c->cfg.n_kv_heads;
+      const int64_t units = (int64_t)batch->n_seqs * c->cfg.n_kv_heads * (((int64_t)batch->table_width * c->cfg.page_size + 63) / 64);
+      if (units < 2 * decode_grid) decode_grid = (int)(units + 1) / 2;
+      a.divide = ctas * shared + decode_grid > a.n_ctas;
+      a.front_ctas = ctas < a.n_ctas ? (int)ctas : a.n_ctas;
+      a.max_splits = shared;
+      a.front_units = (float)(2 * shared_blocks * ((seen + 127) / 128));
+      a.plan = reinterpret_cast<int*>(ws + kPlanOffset);
     }
   }
   if (blocks > 0x7FFFFFFF || shared_blocks > 0x7FFFFFFF) return RQ_ERR_UNSUPPORTED;
@@ -239,10 +237,10 @@ rq_status attention(rq_paged_cache* c, int layer, const rq_paged_batch* batch, c
     rq::PagedAttnArgs f = a;
     f.row_slot = shared;
     if (shared == 0) f.rows_o = f.rows_ml = nullptr;  // straight to out
-    e = rq::launch_paged_decode(c->k16, c->v16, f, d, type, stream);
+    e = rq::launch_paged_decode(c->k16, c->v16, f, decode_grid, d, type, stream);
     a.first = 0;
   };
-  if (side_by_side) run_decode();
+  if (side_by_side) run_decode();  // what it leaves over ends first
   if (e == cudaSuccess && shared > 0) {
     a.over_prefix = 1;
     e = rq::launch_paged_prompt(c->kp, c->vp, a, (int)shared_blocks, shared, d, type, stream);

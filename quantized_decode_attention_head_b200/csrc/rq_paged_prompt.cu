@@ -177,6 +177,8 @@ struct Shared {
   int row_token[kBlockRows];  // packed token, -1: no row
   int row_p[kBlockRows];      // position of the row's query
   int p_min[8], p_max[8];     // of each warp's 32 rows
+  int64_t tail[4];         // units of the decode kernel, by the warp that counted them
+  int splits;
   int dead;
   int bad;  // a page number out of range in the CTA's walk
 };
@@ -200,7 +202,9 @@ __device__ __forceinline__ int key_of(const Keys& k, int tile) {
   return kKeys * (tile < k.ns ? tile : k.lo_t + tile - k.ns);
 }
 
-template <class T, int D>
+// kPrefix: all rows of the batch over the prefix (two kernels: what one of them
+// does not need costs the other registers, which its softmax has none to spare of).
+template <class T, int D, bool kPrefix>
 __global__ void __launch_bounds__(kThreads, 1)
     paged_prompt_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
                         const __grid_constant__ PagedAttnArgs a) {
@@ -225,7 +229,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   // ---- which rows
   int row0 = 0, rows = 0;
   Seq seq = {};
-  if (a.over_prefix) {
+  if (kPrefix) {
     row0 = blockIdx.x * kBlockRows;
     rows = a.b.n_tokens << a.b.g_shift;
   } else {
@@ -296,7 +300,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     int token = -1, p = 0;
     if (r < rows) {
       token = r >> a.b.g_shift;
-      if (a.over_prefix) {
+      if (kPrefix) {
         const int b = seq_of(a.b, token);
         if (b >= 0) {
           const Seq s = load_seq(a.b, b);
@@ -325,9 +329,22 @@ __global__ void __launch_bounds__(kThreads, 1)
       sh.p_max[warp] = hi;
     }
   }
+  if (kPrefix && a.divide && warp >= 8) {
+    int64_t units = 0;
+    for (int b = tid - 256; b < a.b.n_seqs; b += 128) units += walk_of(a, b).units;
+#pragma unroll
+    for (int k = 16; k; k >>= 1) units += __shfl_xor_sync(0xffffffffu, units, k);
+    if (lane == 0) sh.tail[warp - 8] = units;
+    asm volatile("bar.sync 2, 128;\n" ::: "memory");
+    if (tid == 256) {
+      sh.splits = shares_of(a, sh.tail[0] + sh.tail[1] + sh.tail[2] + sh.tail[3]).splits;
+      if (blockIdx.x + blockIdx.y + blockIdx.z == 0) *a.plan = sh.splits;
+    }
+  }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  const int splits = kPrefix && a.divide ? sh.splits : (int)gridDim.z;
   const uint32_t tmem = __shfl_sync(0xffffffffu, sh.tmem, 0);
   int p_lo[2], p_hi[2];
 #pragma unroll
@@ -335,13 +352,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     p_lo[t] = min(min(sh.p_min[4 * t], sh.p_min[4 * t + 1]), min(sh.p_min[4 * t + 2], sh.p_min[4 * t + 3]));
     p_hi[t] = max(max(sh.p_max[4 * t], sh.p_max[4 * t + 1]), max(sh.p_max[4 * t + 2], sh.p_max[4 * t + 3]));
   }
-  const int tiles_q = p_hi[1] != INT_MIN ? 2 : (p_hi[0] != INT_MIN ? 1 : 0);  // row tiles with any row
+  // row tiles with any row; none where the SM is the decode kernel's
+  const int tiles_q = kPrefix && (int)blockIdx.z >= splits ? 0 : (p_hi[1] != INT_MIN ? 2 : (p_hi[0] != INT_MIN ? 1 : 0));
 
   // ---- which keys
   Keys key;
-  key.base = a.over_prefix ? 0 : a.prefix_len;
-  key.end = a.over_prefix ? a.prefix_len : seq.len;
-  key.pages = a.over_prefix ? a.prefix : a.b.table + (int64_t)sh.seq * a.b.width;
+  key.base = kPrefix ? 0 : a.prefix_len;
+  key.end = kPrefix ? a.prefix_len : seq.len;
+  key.pages = kPrefix ? a.prefix : a.b.table + (int64_t)sh.seq * a.b.width;
   {
     const int first = min(p_lo[0], p_lo[1]), last = max(p_hi[0], p_hi[1]);
     int hi = tiles_q ? last + 1 - key.base : 0;
@@ -356,8 +374,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int st = (key.sink + kKeys - 1) / kKeys;
     key.ns = st < key.lo_t ? st : key.lo_t;
     const int n = key.ns + (hi + kKeys - 1) / kKeys - key.lo_t;
-    key.t0 = (int)((int64_t)n * blockIdx.z / gridDim.z);
-    key.t1 = (int)((int64_t)n * (blockIdx.z + 1) / gridDim.z);
+    key.t0 = (int)((int64_t)n * blockIdx.z / splits);
+    key.t1 = (int)((int64_t)n * (blockIdx.z + 1) / splits);
   }
   const int n_steps = key.t1 - key.t0;
 
@@ -522,12 +540,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     // -------------------------------------------------- softmax, one row a thread
     const int t = (warp - 4) / 4;
     const int r = t * kTileRows + (warp & 3) * 32 + lane;
-    const int token = sh.row_token[r], p = sh.row_p[r];
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t s_at = tmem + t * kKeys + lanes, o_at = tmem + 2 * kKeys + t * D + lanes;
-    // keys the row sees: [w_lo, limit) and [0, sink), the latter below limit too
-    const int limit = token >= 0 ? min(key.end, p + 1 - key.base) : 0;
-    const int w_lo = a.window > 0 ? p + 1 - a.window - key.base : 0;
+    // every row of the tile sees all keys of (all_lo, all_end)
+    const int all_end = min(key.end, p_lo[t] + 1 - key.base);
+    const int all_lo = a.window > 0 && p_hi[t] != INT_MIN ? p_hi[t] - a.window - key.base : INT_MIN;
     float m = -INFINITY, l = 0.f;
     bool ok = true;
     for (int k = 0; k < n_steps; ++k) {
@@ -535,11 +552,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       ok = warp_wait(&sh.s_full[t], k & 1);
       if (!ok) break;
       tc_fence_after();
-      const bool whole = !any_bad && j + kKeys <= min(key.end, p_lo[t] + 1 - key.base) &&
-                         (a.window == 0 || j > p_hi[t] - a.window - key.base || j + kKeys <= key.sink);
+      const bool whole = !any_bad && j + kKeys <= all_end && (j > all_lo || j + kKeys <= key.sink);
       if (__any_sync(0xffffffffu, !whole)) {
         // masked in place, 32 columns at a time: a CTA meets one to three such
         // tiles, and code unrolled over 128 columns cost more to fetch than to run
+        // keys the row sees: [w_lo, limit) and [0, sink), the latter below limit too
+        const int p = sh.row_p[r] - key.base;
+        const int limit = sh.row_token[r] >= 0 ? min(key.end, p + 1) : 0;
+        const int w_lo = a.window > 0 ? p + 1 - a.window : 0;
         uint32_t pages = 0xFFu;  // bit g: the page of keys 16 g.. of the tile was loaded
         if (any_bad) {
           pages = 0;
@@ -645,6 +665,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc_fence_after();
     }
     if (!ok) sh.dead = 1;
+    const int token = sh.row_token[r];
     const int64_t row = (int64_t)token * a.b.hq + h * G + ((row0 + r) & (G - 1));
     const int64_t at = (int64_t)(a.row_slot + blockIdx.z) * a.b.n_tokens * a.b.hq + row;
     const float inv = l == 0.f ? 0.f : 1.f / l;
@@ -697,8 +718,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;\n" ::"r"(tmem), "r"(C::COLS));
 }
 
-// Rows whose state lies in parts: slots [0, shared) of every row, then one
-// slot of the decode kernel or `own` slots of the prompt kernel.  One warp a
+// Rows whose state lies in parts: slots [0, shared) of every row (as many of
+// them as the plan says, where the SMs were divided), then, from slot `shared`
+// on, one of the decode kernel or `own` of the prompt kernel.  One warp a
 // row; the parts of a row are read in order, so results do not depend on
 // timing.
 template <class T, int D>
@@ -718,9 +740,11 @@ __global__ void __launch_bounds__(128) paged_merge_kernel(const __grid_constant_
   if (token < s.t0 || token >= s.t0 + s.n) return;  // no sequence's
   const bool few = a.few_rows_apart && (s.n << a.b.g_shift) <= kDecodeRows;
   if (few && shared == 0) return;  // the decode kernel wrote the result
-  const int slots = shared + (few ? 1 : own);
+  const int over = a.divide ? ld_once(a.plan) : shared, skip = shared - over;
+  const int slots = over + (few ? 1 : own);
+  auto slot = [&](int k) { return (int64_t)(k < over ? k : k + skip) * n_rows + row; };
   float M = -INFINITY;
-  for (int k = lane; k < slots; k += 32) M = fmaxf(M, ld_once(a.rows_ml + 2 * (k * n_rows + row)));
+  for (int k = lane; k < slots; k += 32) M = fmaxf(M, ld_once(a.rows_ml + 2 * slot(k)));
 #pragma unroll
   for (int k = 16; k; k >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, k));
   const float mu = M == -INFINITY ? 0.f : M;
@@ -732,7 +756,7 @@ __global__ void __launch_bounds__(128) paged_merge_kernel(const __grid_constant_
   // (a part that saw nothing holds zeros and the maximum -inf: weight 0)
 #pragma unroll 16
   for (int k = 0; k < slots; ++k) {
-    const int64_t at = k * n_rows + row;
+    const int64_t at = slot(k);
     const float2 x = ld_once(reinterpret_cast<const float2*>(a.rows_ml + 2 * at));
     const float f = ex2(x.x - mu);
     L = fmaf(f, x.y, L);
@@ -759,7 +783,9 @@ template <class T, int D>
 cudaError_t launch(const CUtensorMap& km, const CUtensorMap& vm, const PagedAttnArgs& a, int blocks, int splits,
                    cudaStream_t s) {
   static_assert(Cfg<D>::SMEM + sizeof(Shared) + 64 <= 227 * 1024, "shared memory");
-  return launch_pdl<paged_prompt_kernel<T, D>>(dim3(blocks, a.b.hkv, splits), kThreads, Cfg<D>::SMEM, s, km, vm, a);
+  const dim3 grid(blocks, a.b.hkv, splits);
+  return a.over_prefix ? launch_pdl<paged_prompt_kernel<T, D, true>>(grid, kThreads, Cfg<D>::SMEM, s, km, vm, a)
+                       : launch_pdl<paged_prompt_kernel<T, D, false>>(grid, kThreads, Cfg<D>::SMEM, s, km, vm, a);
 }
 
 template <class T, int D>

@@ -346,3 +346,57 @@ def place(bt, pages, rows):
             full[:, :n] = part
             blocks = full.view(bt.hkv, -1, bt.page, bt.d).transpose(0, 1)
             pages[0, numbers[: blocks.shape[0]].long()] = blocks.to(pages.device)
+
+
+# ------------------------------------------- how the SMs and keys are divided
+@pytest.mark.parametrize("lens,prefix", [
+    ([(40 + 37 * i % 300, 1) for i in range(24)], 9000), ([(300, 2)] * 5, 2000), ([(3000, 1)] * 40, 700),
+    ([(20 + i % 90, 1) for i in range(300)], 5000), ([(0, 1), (0, 1)], 4000)])
+@pytest.mark.parametrize("window,n_sink", [(0, 0), (600, 4)])
+def test_a_wider_table_changes_nothing(lens, prefix, window, n_sink):
+    """A captured call keeps its table at the longest length it may meet: the
+    division of the SMs between the prefix and what follows it goes by the
+    lengths, so results are the same bit for bit."""
+    bt = Batch(lens, 8, 2, 64, 16, BF, seed=81, prefix=prefix)
+    ref = reference(bt, window, n_sink)
+    cache = make(bt)
+    ws = cache.make_workspace(len(lens), bt.rows)
+    got = []
+    for wide in (1, 16, 300):
+        table = torch.full((len(lens), wide * bt.table.shape[1]), -1, dtype=torch.int32, device="cuda")
+        table[:, : bt.table.shape[1]] = bt.table
+        lse = torch.empty((bt.rows, 8), device="cuda")
+        out = cache.rq_paged_shared_attention(0, bt.q, bt.prefix_pages, prefix, table, bt.kv_lens, cu_new=bt.cu,
+                                              max_new=bt.max_new, window=window, n_sink=n_sink, lse=lse, workspace=ws)
+        check(bt, out, ref)
+        check_lse(bt, lse, ref)
+        got.append((out, lse))
+    assert cache.read_status(ws) == 0
+    for out, lse in got[1:]:
+        assert torch.equal(out, got[0][0]) and torch.equal(lse, got[0][1])
+
+
+def test_a_captured_call_divides_by_the_lengths_it_finds():
+    """Replayed with lengths that make the tails a small part, then most of the
+    work, and sequences that come and go."""
+    lens = [(4000, 1)] * 20
+    bt = Batch(lens, 8, 2, 64, 32, BF, seed=82, prefix=3000)
+    cache = make(bt)
+    ws = cache.make_workspace(20, bt.rows)
+    lse = torch.empty((bt.rows, 8), device="cuda")
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        attend(bt, cache, lse=lse, workspace=ws)
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = attend(bt, cache, lse=lse, workspace=ws)
+    for kv in ([4000] * 20, [5] * 20, [4000] + [0] * 19, [1 + 200 * i for i in range(20)]):
+        bt.kv_lens.copy_(torch.tensor(kv, dtype=torch.int32))
+        graph.replay()
+        bt.lens = [(n, 1) for n in kv]
+        ref = reference(bt)
+        check(bt, out, ref, str(kv[:2]))
+        check_lse(bt, lse, ref)
+    assert cache.read_status(ws) == 0
