@@ -400,3 +400,24 @@ def test_a_captured_call_divides_by_the_lengths_it_finds():
         check(bt, out, ref, str(kv[:2]))
         check_lse(bt, lse, ref)
     assert cache.read_status(ws) == 0
+
+
+# --------------------------------------------------------- long walks and many parts
+@pytest.mark.parametrize("what,lens,prefix,hq,hkv", [
+    ("prefix in 128 parts", [(50, 1), (9, 1)], 66000, 4, 1),
+    ("prefix in many parts, pieces behind it", [(600, 300), (9, 1), (70, 70)], 20000, 8, 2),
+    ("one piece, its keys in many parts", [(30000, 40)], 0, 4, 1),
+    ("47 tiles in one go", [(6000 - i, 40) for i in range(40)], 0, 4, 4),
+    ("one token, its keys in 296 parts", [(100000, 1)], 0, 8, 1),
+    ("a prompt of 4000 without a window", [(4000, 4000)], 0, 2, 2)])
+@pytest.mark.parametrize("dtype,d", [(BF, 128), (FP, 64)])
+def test_many_parts_and_long_walks(what, lens, prefix, hq, hkv, dtype, d):
+    bt = Batch(lens, hq, hkv, d, 64, dtype, seed=91, prefix=prefix)
+    ref = reference(bt)
+    cache = make(bt)
+    lse = torch.empty((bt.rows, hq), device="cuda")
+    ws = cache.make_workspace(len(lens), bt.rows)
+    for _ in range(2):
+        check(bt, attend(bt, cache, lse=lse, workspace=ws), ref, what)
+        check_lse(bt, lse, ref, what)
+    assert cache.read_status(ws) == 0
