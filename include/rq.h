@@ -283,8 +283,9 @@ rq_status rq_decode_step(rq_cache* cache, int layer, const void* q, const void* 
                          float* out, float softmax_scale, int n_splits, void* workspace, size_t ws_bytes,
                          cudaStream_t stream);
 
-/* Blocking read of the workspace status word: 0 when every kernel that used
- * this workspace completed normally, otherwise RQ_ERR_DEVICE_TIMEOUT in the
+/* Blocking read of the workspace status word, after everything queued on the
+ * current device, on any stream: 0 when every kernel that used this workspace
+ * completed normally, otherwise RQ_ERR_DEVICE_TIMEOUT in the
  * low byte (a pipeline wait gave up after ~1 s and the kernel returned
  * without writing its outputs). */
 rq_status rq_decode_read_status(const void* workspace, int* device_status);

@@ -343,6 +343,8 @@ class PagedKVCache:
                 ctypes.byref(cfg), _dptr(k_pages), _dptr(v_pages), ctypes.byref(handle)))
             # RQ_ERR_DEVICE_INDEX of the appends (attention calls report in their workspace)
             self.append_status = torch.zeros(1, dtype=torch.int32, device=k_pages.device)
+            if not torch.cuda.is_current_stream_capturing():
+                torch.cuda.current_stream().synchronize()  # appends may run on other streams
         self.handle = handle
         self._destroy = lib().rq_paged_cache_destroy
         # the structures that calls fill in, and what a call needs of torch
@@ -559,7 +561,8 @@ class PagedKVCache:
 
     def read_status(self, workspace=None) -> int:
         """Blocking read of the status word of an attention workspace, or
-        (None) of the appends: 0, or RQ_ERR_DEVICE_INDEX / _TIMEOUT."""
-        if workspace is None:
-            return int(self.append_status.item())
-        return QuantizedKVCache.rq_decode_read_status(workspace)
+        (None) of the appends, after the calls queued on any stream of the
+        pages' device: 0, or RQ_ERR_DEVICE_INDEX / _TIMEOUT."""
+        word = self.append_status if workspace is None else workspace
+        with self._device_guard(self.device):
+            return QuantizedKVCache.rq_decode_read_status(word)

@@ -411,6 +411,8 @@ rq_status rq_selftest_device_timeout(void* workspace, size_t ws_bytes, unsigned 
 
 rq_status rq_decode_read_status(const void* workspace, int* device_status) {
   if (!workspace || !device_status) return RQ_ERR_INVALID_ARG;
+  // a copy on the default stream does not wait for streams created without blocking it
+  if (cuda_status(cudaDeviceSynchronize()) != RQ_OK) return RQ_ERR_CUDA;
   return cuda_status(cudaMemcpy(device_status, workspace, sizeof(int), cudaMemcpyDeviceToHost));
 }
 
@@ -532,5 +534,6 @@ extern "C" rq_status rq_decode_noalloc_read_status(int* device_status) {
   if (!device_status) return RQ_ERR_INVALID_ARG;
   void* scratch = nullptr;
   if (cuda_status(rq::noalloc_scratch(&scratch)) != RQ_OK) return RQ_ERR_CUDA;
+  if (cuda_status(cudaDeviceSynchronize()) != RQ_OK) return RQ_ERR_CUDA;  // as rq_decode_read_status
   return cuda_status(cudaMemcpy(device_status, scratch, sizeof(int), cudaMemcpyDeviceToHost));
 }

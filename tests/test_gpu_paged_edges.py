@@ -421,3 +421,40 @@ def test_many_parts_and_long_walks(what, lens, prefix, hq, hkv, dtype, d):
         check(bt, attend(bt, cache, lse=lse, workspace=ws), ref, what)
         check_lse(bt, lse, ref, what)
     assert cache.read_status(ws) == 0
+
+
+# ------------------------------------------------ status of calls on other streams
+def test_status_reads_wait_for_every_stream():
+    """Calls queued on another stream, behind some milliseconds of work, report
+    a page that does not exist to a status read that follows at once."""
+    bt = Batch([(100, 1), (100, 1)], 4, 2, 64, 16, BF, seed=11)
+    cache = make(bt)
+    ws = cache.make_workspace(2, bt.rows)
+    bt.table[1, 6] = 1 << 30
+    new = torch.ones((2, 2, 64), dtype=BF, device="cuda")
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(s):
+        torch.cuda._sleep(20_000_000)
+    attend(bt, cache, workspace=ws, stream=s)
+    assert cache.read_status(ws) == 8
+    with torch.cuda.stream(s):
+        torch.cuda._sleep(20_000_000)
+    cache.rq_paged_append(0, new, new, bt.table, bt.kv_lens, stream=s)
+    assert cache.read_status() == 8
+
+
+def test_a_new_cache_serves_another_stream_at_once():
+    """The status word of the appends is cleared before the constructor
+    returns, however much is queued on the current stream."""
+    bt = Batch([(100, 1), (100, 1)], 4, 2, 64, 16, BF, seed=11)
+    bt.table[1, 6] = 1 << 30
+    new = torch.ones((2, 2, 64), dtype=BF, device="cuda")
+    make(bt).rq_paged_append(0, new, new, bt.table, bt.kv_lens)
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    torch.cuda._sleep(20_000_000)
+    cache = make(bt)
+    cache.rq_paged_append(0, new, new, bt.table, bt.kv_lens, stream=s)
+    torch.cuda.synchronize()
+    assert cache.read_status() == 8
