@@ -65,6 +65,13 @@ def _same_device(name, t, device):
         raise ValueError(f"{name} must be on the device of the pages")
 
 
+def _int32(**values):
+    """ctypes cuts what does not fit; called where a shift shows bits past it (or a sign)."""
+    for name, v in values.items():
+        if not -(2**31) <= v < 2**31:
+            raise ValueError(f"{name} = {v} does not fit 32 bits")
+
+
 def rq_allocate_bits(w, alpha, beta, avg_bits, allowed):
     """RateQuant allocation (host).  Returns dict(b_cont, b_int, log_lambda)."""
     w = np.ascontiguousarray(w, dtype=np.float64)
@@ -333,6 +340,7 @@ class PagedKVCache:
         self.k_pages, self.v_pages = k_pages, v_pages
         self.n_layers, self.n_pages, self.n_kv_heads, self.page_size, self.head_dim = k_pages.shape
         self.n_q_heads = int(n_q_heads)
+        _int32(n_q_heads=self.n_q_heads)
         self.dtype = k_pages.dtype
         self.device = k_pages.get_device()
         cfg = PagedConfig(self.n_layers, self.n_pages, self.page_size, self.n_q_heads, self.n_kv_heads,
@@ -391,6 +399,8 @@ class PagedKVCache:
             b.cu_new, b.max_new = None, 1
         else:
             b.cu_new = self._ints("cu_new", cu_new, (n_seqs + 1,))
+            if max_new is not None and max_new >> 31:
+                _int32(max_new=max_new)
             b.max_new = n_tokens if max_new is None else max_new
         return n_seqs
 
@@ -450,6 +460,8 @@ class PagedKVCache:
         if v_new.shape[0] != n:
             raise ValueError(f"v_new has {v_new.shape[0]} tokens, k_new {n}")
         self._batch(n, page_table, kv_lens, cu_new, None)
+        if layer >> 31:
+            _int32(layer=layer)
         rot, qs, q_ptr, out_ptr = None, 0, None, None
         if cos_sin is None:
             if q is not None or positions is not None or sections is not None:
@@ -475,6 +487,9 @@ class PagedKVCache:
                 sections = (rot.rot_dim // 2,)
             if len(sections) != axes:
                 raise ValueError(f"{len(sections)} sections for positions on {axes} axes")
+            for pairs in sections:
+                if pairs >> 31:
+                    _int32(sections=pairs)
             rot.n_axes = axes
             rot.sections[:axes] = sections
             if q is not None:
@@ -492,6 +507,7 @@ class PagedKVCache:
         return q_out
 
     def rq_paged_workspace_bytes(self, n_seqs, n_tokens) -> int:
+        _int32(n_seqs=n_seqs, n_tokens=n_tokens)
         out = ctypes.c_size_t(0)
         check("rq_paged_workspace_bytes", lib().rq_paged_workspace_bytes(self.handle, n_seqs, n_tokens,
                                                                          ctypes.byref(out)))
@@ -541,6 +557,8 @@ class PagedKVCache:
         qs = self._packed("q", q, self.n_q_heads)
         n = q.shape[0]
         n_seqs = self._batch(n, page_table, kv_lens, cu_new, max_new)
+        if (layer | window | n_sink) >> 31:
+            _int32(layer=layer, window=window, n_sink=n_sink)
         if out is None:
             out = self._new_like(q, stream)
         else:

@@ -458,3 +458,26 @@ def test_a_new_cache_serves_another_stream_at_once():
     cache.rq_paged_append(0, new, new, bt.table, bt.kv_lens, stream=s)
     torch.cuda.synchronize()
     assert cache.read_status() == 8
+
+
+# ------------------------------------------------------------------ refusals
+def test_integers_past_32_bits_are_refused():
+    """They would reach the C call cut to 32 bits: a window of 2^32 + 10 as 10."""
+    bt = Batch([(20, 1), (5, 1)], 4, 2, 64, 16, BF)
+    cache = make(bt)
+    big = 2**32 + 10
+    for kw in (dict(window=big), dict(n_sink=big), dict(max_new=big), dict(window=-big), dict(window=2**31)):
+        with pytest.raises(ValueError, match="32 bits"):
+            cache.rq_paged_attention(0, bt.q, bt.table, bt.kv_lens, cu_new=bt.cu, **kw)
+    for layer in (2**32, -(2**32)):
+        with pytest.raises(ValueError, match="32 bits"):
+            cache.rq_paged_attention(layer, bt.q, bt.table, bt.kv_lens)
+        with pytest.raises(ValueError, match="32 bits"):
+            cache.rq_paged_append(layer, bt.q[:, :2], bt.q[:, :2], bt.table, bt.kv_lens)
+    with pytest.raises(ValueError, match="32 bits"):
+        cache.make_workspace(2**32, 4)
+    with pytest.raises(ValueError, match="32 bits"):
+        PagedKVCache(bt.k_pages, bt.v_pages, 2**32 + 4)
+    with pytest.raises(ValueError, match="32 bits"):
+        cache.rq_paged_append(0, bt.q[:, :2], bt.q[:, :2], bt.table, bt.kv_lens, cos_sin=angles(64, 64),
+                              sections=[2**32 + 32])
