@@ -41,13 +41,12 @@ struct PagedAppendArgs {
   const int* positions;
   int n_positions, rot, interleaved, n_axes;
   int sections[kMaxAxes];
+  int sms;
   int block_tokens;  // tokens of a block (set by the launch)
 };
 
 struct PagedAttnArgs {
   PagedBatch b;
-  const uint16_t* k_pages;
-  const uint16_t* v_pages;
   const uint16_t* q;
   int64_t q_stride;
   uint16_t* out;

@@ -105,28 +105,6 @@ __device__ __forceinline__ Place place_of(const PagedAppendArgs& a, int64_t t64)
 
 // kPairs: channels j and j + rot/2 are paired (else 2j and 2j + 1).
 template <class T, int D, bool kPairs>
-__device__ __forceinline__ void move_tokens(const PagedAppendArgs& a, const Place* places, int64_t t0);
-
-// kPairs: channels j and j + rot/2 are paired (else 2j and 2j + 1).
-template <class T, int D, bool kPairs>
-__global__ void __launch_bounds__(kThreads + 32, kResident) paged_append_kernel(const __grid_constant__ PagedAppendArgs a) {
-  griddep_wait();
-  griddep_launch_dependents();
-  __shared__ Place places[2][kMaxTokens];
-  const int tokens = a.block_tokens, stride = gridDim.x * tokens;
-  const int finder = (int)threadIdx.x - kThreads;  // lane of the warp that finds places
-  int64_t t0 = (int64_t)blockIdx.x * tokens;
-  if (finder >= 0 && finder < tokens) places[0][finder] = place_of(a, t0 + finder);
-  for (int turn = 0; t0 < a.b.n_tokens; t0 += stride, turn ^= 1) {
-    __syncthreads();
-    if (finder < 0)
-      move_tokens<T, D, kPairs>(a, places[turn], t0);
-    else if (finder < tokens)
-      places[turn ^ 1][finder] = place_of(a, t0 + stride + finder);
-  }
-}
-
-template <class T, int D, bool kPairs>
 __device__ __forceinline__ void move_tokens(const PagedAppendArgs& a, const Place* places, int64_t t0) {
   const int tokens = a.block_tokens;
   const int rot = a.cos_sin ? a.rot : 0, half = rot / 2;
@@ -216,14 +194,32 @@ __device__ __forceinline__ void move_tokens(const PagedAppendArgs& a, const Plac
   }
 }
 
+template <class T, int D, bool kPairs>
+__global__ void __launch_bounds__(kThreads + 32, kResident) paged_append_kernel(const __grid_constant__ PagedAppendArgs a) {
+  griddep_wait();
+  griddep_launch_dependents();
+  __shared__ Place places[2][kMaxTokens];
+  const int tokens = a.block_tokens, stride = gridDim.x * tokens;
+  const int finder = (int)threadIdx.x - kThreads;  // lane of the warp that finds places
+  int64_t t0 = (int64_t)blockIdx.x * tokens;
+  if (finder >= 0 && finder < tokens) places[0][finder] = place_of(a, t0 + finder);
+  for (int turn = 0; t0 < a.b.n_tokens; t0 += stride, turn ^= 1) {
+    __syncthreads();
+    if (finder < 0)
+      move_tokens<T, D, kPairs>(a, places[turn], t0);
+    else if (finder < tokens)
+      places[turn ^ 1][finder] = place_of(a, t0 + stride + finder);
+  }
+}
+
 template <class T, int D>
 cudaError_t launch(PagedAppendArgs a, cudaStream_t s) {
   // tokens of a block: 8 when that still leaves four blocks an SM
   static_assert(kMaxTokens * D / 8 <= kThreads, "one lane an item at least");
   a.block_tokens = 1;
-  while (a.block_tokens < kMaxTokens && a.b.n_tokens / (2 * a.block_tokens) >= 4 * 148) a.block_tokens *= 2;
+  while (a.block_tokens < kMaxTokens && a.b.n_tokens / (2 * a.block_tokens) >= 4 * a.sms) a.block_tokens *= 2;
   int64_t blocks = (a.b.n_tokens + (int64_t)a.block_tokens - 1) / a.block_tokens;
-  if (a.block_tokens == kMaxTokens && blocks > kResident * 148) blocks = kResident * 148;  // one wave, several rounds each
+  if (a.block_tokens == kMaxTokens && blocks > kResident * a.sms) blocks = kResident * a.sms;  // one wave, several rounds each
   const dim3 grid((unsigned)blocks);
   return a.interleaved ? launch_pdl<paged_append_kernel<T, D, false>>(grid, kThreads + 32, 0, s, a)
                        : launch_pdl<paged_append_kernel<T, D, true>>(grid, kThreads + 32, 0, s, a);

@@ -100,18 +100,27 @@ bool encode(EncodeTiled fn, const rq_paged_cache* c, void* base, int box_rows, i
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// Tensor maps of the pages and the device's size, at the first attention call.
+// The device's size, at the first call.
+rq_status find_sms(rq_paged_cache* c) {
+  if (c->sms > 0) return RQ_OK;
+  int dev = 0, sms = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  if (e != cudaSuccess) return cuda_status(e);
+  c->sms = sms;
+  return RQ_OK;
+}
+
+// The tensor maps of the pages too, at the first attention call.
 rq_status prepare(rq_paged_cache* c) {
   if (c->mapped) return RQ_OK;
+  const rq_status st = find_sms(c);
+  if (st != RQ_OK) return st;
   void* fn = nullptr;
   cudaDriverEntryPointQueryResult found;
   const cudaError_t e = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault, &found);
   if (e != cudaSuccess) return cuda_status(e);
   if (!fn || found != cudaDriverEntryPointSuccess) return cuda_status(cudaErrorNotSupported);
-  int dev = 0;
-  cudaError_t d = cudaGetDevice(&dev);
-  if (d == cudaSuccess) d = cudaDeviceGetAttribute(&c->sms, cudaDevAttrMultiProcessorCount, dev);
-  if (d != cudaSuccess) return cuda_status(d);
   const EncodeTiled enc = reinterpret_cast<EncodeTiled>(fn);
   const int page = c->cfg.page_size, panels = c->cfg.head_dim / 64;
   if (!encode(enc, c, c->k, 16, panels, &c->k16) || !encode(enc, c, c->v, 16, panels, &c->v16) ||
@@ -168,8 +177,6 @@ rq_status attention(rq_paged_cache* c, int layer, const rq_paged_batch* batch, c
   a.n_ctas = decode_ctas(c);
   a.few_rows_only = (int64_t)batch->max_new << c->g_shift <= rq::kDecodeRows;
   a.b.status = static_cast<int*>(workspace);
-  a.k_pages = c->k;
-  a.v_pages = c->v;
   a.q = static_cast<const uint16_t*>(q);
   a.q_stride = q_stride;
   a.out = static_cast<uint16_t*>(out);
@@ -321,6 +328,9 @@ rq_status rq_paged_append(rq_paged_cache* c, int layer, const rq_paged_batch* ba
     a.n_axes = rot->n_axes;
   }
   if (batch->n_tokens == 0 || batch->n_seqs == 0) return RQ_OK;
+  const rq_status sized = find_sms(c);
+  if (sized != RQ_OK) return sized;
+  a.sms = c->sms;
   a.b.status = dev_status;
   a.k_pages = c->k;
   a.v_pages = c->v;
