@@ -395,7 +395,8 @@ void rq_paged_cache_destroy(rq_paged_cache* cache);
 typedef struct {
   int n_seqs;            /* >= 0 */
   int n_tokens;          /* rows of the packed tensors */
-  int max_new;           /* no sequence has more new tokens than this */
+  int max_new;           /* no sequence has more new tokens than this.  Attention chooses its kernels by
+                            it: with max_new * G <= 16 the call has one kernel (a shared prefix: three) */
   int table_width;       /* entries of a row of page_table, >= 1 */
   const int* page_table; /* device [n_seqs][table_width] */
   const int* kv_lens;    /* device [n_seqs] */
@@ -449,18 +450,26 @@ rq_status rq_paged_workspace_bytes(const rq_paged_cache* cache, int n_seqs, int 
  *   one layer, which hold their keys already.  Query i of sequence b stands
  *   at p = kv_lens[b] - n_b + i and sees key j when
  *     j <= p and (window == 0 or p - j < window or j < n_sink).
- *   out = sum_j exp(s q.k_j) v_j / sum_j exp(s q.k_j), accumulated in fp32
- *   and rounded once; 0 for a query that sees nothing.  Query head h reads kv
- *   head h / G.  What lies in the pages at tokens that no query of the
- *   sequence sees (behind its end, before its window) does not matter, NaN
- *   included; a value that is not finite and that some query of the call sees
- *   may reach the results of the call's other queries.
+ *   out = sum_j exp(s q.k_j) v_j / sum_j exp(s q.k_j); 0 for a query that
+ *   sees nothing.  Scores, maxima and sums are fp32, the result is rounded
+ *   once.  The weights exp(..) of a sequence with at most 16 query rows a kv
+ *   head (new tokens x G) are held to 2^-16; with more rows, and for every
+ *   row over a shared prefix, each is rounded once to the type, which makes
+ *   the result's error about 1.4 times that of its own rounding (rms).  Query
+ *   head h reads kv head h / G.
+ *   What lies in the pages at tokens that no query of the sequence sees
+ *   (behind its end, before its window) does not matter, NaN included.  A
+ *   value that is not finite makes the result of a query that sees it not
+ *   finite (infinities may become NaN), and may do so to other queries of the
+ *   sequence (in a shared prefix: of the batch) that do not see it.
  * q: [n_tokens][n_q_heads][head_dim], tokens q_stride elements apart.  out:
  *   contiguous, same type.  lse: nullable fp32 [n_tokens][n_q_heads], the
  *   natural logarithm of the denominator (-inf where nothing is seen), with
  *   which results over parts of the keys can be merged.
  * softmax_scale <= 0 selects 1/sqrt(head_dim).
- * Errors: RQ_ERR_INVALID_ARG, RQ_ERR_WORKSPACE, RQ_ERR_CUDA. */
+ * Errors: RQ_ERR_INVALID_ARG, RQ_ERR_WORKSPACE, RQ_ERR_UNSUPPORTED (positions
+ *   past 31 bits: prefix_len + table_width * page_size + n_tokens, or n_tokens
+ *   from 2^28 on), RQ_ERR_CUDA. */
 rq_status rq_paged_attention(rq_paged_cache* cache, int layer, const rq_paged_batch* batch, const void* q,
                              int64_t q_stride, void* out, float* lse, float softmax_scale, int window, int n_sink,
                              void* workspace, size_t ws_bytes, cudaStream_t stream);

@@ -529,11 +529,13 @@ class PagedKVCache:
         """Causal attention of the batch's new tokens q [tokens, n_q_heads,
         head_dim] over the pages of one layer, which hold their keys and values
         already.  max_new: the most new tokens any sequence has (default: all
-        of q's).  window: a query sees the last `window` tokens up to itself
+        of q's; give it with cu_new where sequences have few new tokens each,
+        or the call launches the kernels of prompts too).  window: a query sees the last `window` tokens up to itself
         and the sequence's first n_sink (0: all tokens).  Returns out, in q's
         type; rows behind the last sequence are left as they were.  lse: fp32
         [tokens, n_q_heads], filled with the natural logarithm of each
-        softmax's denominator."""
+        softmax's denominator.  Without a workspace the call makes one, whose
+        status word nobody can read."""
         return self._attention("rq_paged_attention", self._attention_fns[0], (), layer, q, page_table, kv_lens, cu_new, max_new, window,
                                n_sink, softmax_scale, out, lse, workspace, stream)
 
