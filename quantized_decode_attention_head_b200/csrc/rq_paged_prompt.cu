@@ -754,23 +754,35 @@ __global__ void __launch_bounds__(128) paged_merge_kernel(const __grid_constant_
   float v[E];
 #pragma unroll
   for (int e = 0; e < E; ++e) v[e] = 0.f;
-  // (a part that saw nothing holds zeros and the maximum -inf: weight 0)
-#pragma unroll 16
-  for (int k = 0; k < slots; ++k) {
-    const int64_t at = slot(k);
-    const float2 x = ld_once(reinterpret_cast<const float2*>(a.rows_ml + 2 * at));
-    const float f = ex2(x.x - mu);
-    L = fmaf(f, x.y, L);
-    if constexpr (E == 4) {
-      const float4 o = ld_once(reinterpret_cast<const float4*>(a.rows_o + at * D) + lane);
-      v[0] = fmaf(f, o.x, v[0]);
-      v[1] = fmaf(f, o.y, v[1]);
-      v[2] = fmaf(f, o.z, v[2]);
-      v[3] = fmaf(f, o.w, v[3]);
-    } else {
-      const float2 o = ld_once(reinterpret_cast<const float2*>(a.rows_o + at * D) + lane);
-      v[0] = fmaf(f, o.x, v[0]);
-      v[1] = fmaf(f, o.y, v[1]);
+  // (a part that saw nothing holds zeros and the maximum -inf: weight 0); eight
+  // parts' loads in flight at once
+  constexpr int kAtOnce = 8;
+  for (int k0 = 0; k0 < slots; k0 += kAtOnce) {
+    float2 x[kAtOnce];
+    float o[kAtOnce][E];
+#pragma unroll
+    for (int i = 0; i < kAtOnce; ++i) {
+      x[i] = make_float2(-INFINITY, 0.f);
+#pragma unroll
+      for (int e = 0; e < E; ++e) o[i][e] = 0.f;
+      if (k0 + i < slots) {
+        const int64_t at = slot(k0 + i);
+        x[i] = ld_once(reinterpret_cast<const float2*>(a.rows_ml + 2 * at));
+        if constexpr (E == 4) {
+          const float4 y = ld_once(reinterpret_cast<const float4*>(a.rows_o + at * D) + lane);
+          o[i][0] = y.x, o[i][1] = y.y, o[i][2] = y.z, o[i][3] = y.w;
+        } else {
+          const float2 y = ld_once(reinterpret_cast<const float2*>(a.rows_o + at * D) + lane);
+          o[i][0] = y.x, o[i][1] = y.y;
+        }
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < kAtOnce; ++i) {
+      const float f = ex2(x[i].x - mu);
+      L = fmaf(f, x[i].y, L);
+#pragma unroll
+      for (int e = 0; e < E; ++e) v[e] = fmaf(f, o[i][e], v[e]);
     }
   }
   const float inv = L == 0.f ? 0.f : 1.f / L;
