@@ -379,6 +379,23 @@ def test_a_wider_table_changes_nothing(lens, prefix, window, n_sink):
         assert torch.equal(out, got[0][0]) and torch.equal(lse, got[0][1])
 
 
+@pytest.mark.parametrize("n", [1, 2])
+@pytest.mark.parametrize("kv", [30, 400])
+def test_a_prefix_that_fills_the_device(n, kv):
+    """More blocks of rows over the prefix than SMs: nothing is split, and what
+    follows the prefix has all SMs."""
+    lens = [(max(n, (i * 7) % kv), n) for i in range(700 // n)]
+    bt = Batch(lens, 64, 8, 64, 16, BF, seed=83, prefix=300)
+    ref = reference(bt)
+    cache = make(bt)
+    lse = torch.empty((bt.rows, 64), device="cuda")
+    ws = cache.make_workspace(len(lens), bt.rows)
+    for _ in range(2):
+        check(bt, attend(bt, cache, lse=lse, workspace=ws), ref)
+        check_lse(bt, lse, ref)
+    assert cache.read_status(ws) == 0
+
+
 def test_a_captured_call_divides_by_the_lengths_it_finds():
     """Replayed with lengths that make the tails a small part, then most of the
     work, and sequences that come and go."""
