@@ -27,8 +27,8 @@
 // rounding out of the result.
 //
 // Measured (32/8 heads, D = 128, bf16): 64 ragged sequences up to 8192 tokens
-// 141 us, 5.8 TB/s; one of 131072 tokens 94 us, 5.7 TB/s; 16 with a window of
-// 4096 53 us, 4.7 TB/s.  About 5 us pass before the first keys arrive and 2 at
+// 142 us, 5.8 TB/s; one of 131072 tokens 94 us, 5.7 TB/s; 16 with a window of
+// 4096 55 us, 4.5 TB/s.  About 5 us pass before the first keys arrive and 2 at
 // the end; between them DRAM runs at about 7 TB/s, and the SMs finish their
 // equal shares up to 15 % apart.  One team of four warps and 32-token stages:
 // 148, 90 and 52 us; one team with 16-token stages: 191, 119 and 64 us.

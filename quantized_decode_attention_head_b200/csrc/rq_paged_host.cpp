@@ -219,9 +219,9 @@ rq_status attention(rq_paged_cache* c, int layer, const rq_paged_batch* batch, c
       // the decode kernel's no larger than its units if all lengths were the
       // tables'.  Where both fit there is nothing to divide (a small call: 14
       // us for 15.5).  Else they divide the SMs by the lengths they find, and
-      // blocks left over end at once: 64 sequences behind 32768 tokens take 69
-      // us however wide the table; divided by the table's width they took 68
-      // where it was twice the lengths, 231 where it was 32 times.
+      // blocks left over end at once: 64 sequences behind 32768 tokens take 66
+      // us however wide the table; divided by the table's width they took 65
+      // with the narrowest table, 231 with one 16 times as wide.
       const int64_t ctas = shared_blocks * c->cfg.n_kv_heads;
       const int64_t units = (int64_t)batch->n_seqs * c->cfg.n_kv_heads * (((int64_t)batch->table_width * c->cfg.page_size + 63) / 64);
       if (units < 2 * decode_grid) decode_grid = (int)(units + 1) / 2;

@@ -22,8 +22,9 @@
 //
 // Bound.  At D = 128 a step (256 rows, 128 keys) is 2048 clocks of tensor work
 // and as many of exponentials (16 a clock an SM).  Measured (8192-token prompt,
-// 4096-token window, 32/8 heads): 410 us, 1007 TFLOP/s of visible pairs (461 us in
-// a loop of seconds, at the 1 kW power cap), about 3400 clocks a step.  With the softmax taken out the step still takes 2830:
+// 4096-token window, 32/8 heads, in a loop, at the 1 kW power cap): 450 to 460 us,
+// 895 TFLOP/s of visible pairs, about 3400 clocks a step.  With the softmax taken
+// out the step still takes 2830:
 // queries, keys and values read by the MMAs and written by TMA are 256 KB of
 // shared-memory traffic, 128 bytes a clock; the rest is TMEM traffic of the
 // softmax beside the MMAs.  A block starts in about 5 us (rows, first keys)
