@@ -13,7 +13,7 @@
 // tiles, so one tile's products run while the other's weights are computed.
 // P_t overwrites S_t (16-bit pairs, half its columns).  TMEM columns:
 // [S_0 | S_1 | O_0 | O_1].  The running maximum moves only when a row's scores
-// exceed it by 2^8 (fp16: 2^4), so O is rarely rescaled.  Weights are rounded
+// exceed it by 2^8, so O is rarely rescaled.  Weights are rounded
 // once to 16 bits, half a step of the type, where they enter the product.  A
 // second term fits the columns that P leaves free and makes the error that of
 // the result's own rounding (8192-token prompt: rms 1.08e-4, with one term
